@@ -65,7 +65,8 @@ typedef void *parallax_stream_t; /* a cudaStream_t */
 
 typedef enum {
     PARALLAX_F32 = 0,  /* IEEE binary32 */
-    PARALLAX_BF16 = 1  /* bfloat16 */
+    PARALLAX_BF16 = 1, /* bfloat16 */
+    PARALLAX_E4M3 = 2  /* e4m3 codes with block exponents (paged caches only) */
 } parallax_dtype_t;
 
 typedef enum {
@@ -288,6 +289,116 @@ PARALLAX_API int parallax_decode_noalloc(const void *q, const void *rho, const v
                                          const void *vcache, const int *seqlens, void *y, float *lse,
                                          int B, int H, int Tcap, int d, int in_dtype, int out_dtype,
                                          parallax_stream_t stream);
+
+/*
+ * The 8-bit paged cache.  kpages and vpages [num_pages, Hkv, page_size, d] hold
+ * e4m3 codes (the finite-only 8-bit float: 4 exponent and 3 mantissa bits, largest
+ * value 448, code 0x7f NaN), and kexp, vexp [num_pages, Hkv, page_size / 16] one
+ * signed byte per block of 16 tokens and KV head:
+ *     value = code * 2^exp,  exp in [-120, 120].
+ * parallax_kv_append writes it, parallax_decode_paged_q8 attends to it,
+ * parallax_kv_evict drops the tokens that attention has not looked at.  The
+ * append and the eviction also serve the bf16 cache of parallax_decode_paged
+ * (cache_dtype PARALLAX_BF16, kexp and vexp NULL); parallax_decode_paged_acc
+ * attends to that cache and accumulates weights.
+ *
+ * The weight accumulator wacc [B, Hkv, max_pages * page_size] fp32 belongs to the
+ * caller's sequences, not to the pages (a page that two sequences share has a
+ * weight in each).  Pages that a call writes must be reached by one sequence
+ * only, and once; pages that are only read may be shared.  Nothing checks that.
+ */
+
+/*
+ * parallax_decode_paged_q8 -- parallax_decode_paged over the 8-bit cache, with
+ * or without a probe, optionally accumulating attention weights.
+ *
+ * The operator per query head is the one of parallax_decode on the values the
+ * cache stands for (zubnet.ai news item on Parallax, paragraph 2); the pages
+ * describe no 8-bit cache.
+ *   rho  : [B, Hq, d] bf16, or NULL for softmax attention (y = o).
+ *   kexp, vexp : see above; an exponent below -120 may be read as -120 or less.
+ *   wacc : NULL, or fp32 [B, Hkv, max_pages * page_size]: for t < seqlens[b],
+ *          wacc[b, h, t] += sum over the KV head's query heads of the softmax
+ *          weight s_t.  Other entries are not touched.  16-byte aligned.
+ *   Everything else as parallax_decode_paged.  |k.rho| < 65504.
+ * Results do not depend on the schedule (no atomics).  Scratch: split partials,
+ * and with wacc 4 bytes per (sequence, token slot of the table, query head
+ * rounded up to a multiple of 4, of 8 without rho or above 4 per KV head).
+ */
+PARALLAX_API int parallax_decode_paged_q8(const void *q, const void *rho, const void *kpages, const void *vpages,
+                                          const signed char *kexp, const signed char *vexp, const int *block_table,
+                                          const int *seqlens, void *y, float *lse, float *wacc, int B, int Hq,
+                                          int Hkv, int page_size, int max_pages, int num_pages, int d, int in_dtype,
+                                          int out_dtype, parallax_stream_t stream);
+
+/*
+ * parallax_decode_paged_acc -- the same over the bf16 cache of
+ * parallax_decode_paged; wacc is required, rho may be NULL.
+ */
+PARALLAX_API int parallax_decode_paged_acc(const void *q, const void *rho, const void *kpages, const void *vpages,
+                                           const int *block_table, const int *seqlens, void *y, float *lse,
+                                           float *wacc, int B, int Hq, int Hkv, int page_size, int max_pages,
+                                           int num_pages, int d, int in_dtype, int out_dtype,
+                                           parallax_stream_t stream);
+
+/*
+ * parallax_kv_append -- new keys and values behind the last token of each
+ * sequence (a prompt, a chunk of one, or the token of a decode step).
+ *
+ *   k, v        : bf16; element (b, h, t, i) at b s[0] + h s[1] + t s[2] + i of
+ *                 HOST arrays k_strides, v_strides (elements, multiples of 8),
+ *                 NULL for a dense [B, Hkv, T, d].
+ *   seqlens     : DEVICE int32 [B], tokens already in the cache.
+ *   counts      : DEVICE int32 [B], new tokens of each sequence, 0 <= counts[b]
+ *                 <= T; NULL for T each.
+ *   new_seqlens : DEVICE int32 [B] or NULL (written: seqlens + counts); another
+ *                 array than seqlens and counts (PARALLAX_ERR_UNSUPPORTED).
+ *   wacc        : NULL, or the accumulator: the new tokens' entries become 0.
+ *   Token t goes to row t % page_size of page block_table[b, t / page_size].
+ *   8-bit cache: a block takes the smallest exponent e >= that of its rows that
+ *   are there already with |x| <= 448 2^e for every new row; new rows are rounded
+ *   to nearest even, rows that are there are moved to e (exact while their code
+ *   does not become subnormal).  An element that is not finite is stored as NaN
+ *   and does not enter e.
+ *   Rows of no new token are not touched.  Tokens past max_pages * page_size are
+ *   dropped, and tokens of a page id outside [0, num_pages) too; both set
+ *   PARALLAX_ERR_DEVICE_INDEX in the device error word.  No scratch.
+ */
+PARALLAX_API int parallax_kv_append(const void *k, const void *v, const long long *k_strides,
+                                    const long long *v_strides, void *kpages, void *vpages, signed char *kexp,
+                                    signed char *vexp, const int *block_table, const int *seqlens, const int *counts,
+                                    int *new_seqlens, float *wacc, int B, int Hkv, int T, int page_size,
+                                    int max_pages, int num_pages, int d, int in_dtype, int cache_dtype,
+                                    parallax_stream_t stream);
+
+/*
+ * parallax_kv_evict -- keep the newest and the most attended tokens.
+ *
+ * Per sequence (L = seqlens[b] tokens) and KV head, n = min(L, budget) tokens
+ * stay: the newest min(recent, n), and of the others those with the largest
+ * wacc (equal weights: the lower position first; NaN as -inf).  In their order
+ * they become tokens 0 .. n-1 of the pages that new_table names; the pages of
+ * block_table are only read, so the caller gives those back afterwards.
+ *
+ *   new_table   : DEVICE int32 [B, new_max_pages]: pages that no entry of
+ *                 block_table reaches.  Another array than block_table.
+ *   new_seqlens : DEVICE int32 [B] (written: n).
+ *   kept        : DEVICE int32 [B, Hkv, budget] (written up to n): the old
+ *                 position of each kept token.
+ *   new_wacc    : NULL, or fp32 [B, Hkv, new_max_pages * page_size] (written up
+ *                 to n): the kept tokens' weights.
+ *   1 <= budget <= new_max_pages * page_size; 0 <= recent <= budget.
+ *   8-bit cache: a new block takes the largest exponent of its rows' old blocks.
+ *   Rows past n are not touched.  A row of a page id outside [0, num_pages) is
+ *   kept as zero, a new page outside it is not written; both set
+ *   PARALLAX_ERR_DEVICE_INDEX.  new_seqlens, new_wacc and new_table equal to
+ *   their counterparts: PARALLAX_ERR_UNSUPPORTED.  No scratch.
+ */
+PARALLAX_API int parallax_kv_evict(void *kpages, void *vpages, signed char *kexp, signed char *vexp,
+                                   const int *block_table, const int *seqlens, const float *wacc,
+                                   const int *new_table, int *new_seqlens, int *kept, float *new_wacc, int B,
+                                   int Hkv, int page_size, int max_pages, int new_max_pages, int num_pages, int d,
+                                   int budget, int recent, int cache_dtype, parallax_stream_t stream);
 
 /*
  * parallax_rho_proj -- the learned probe rho = x W_R, split per head.

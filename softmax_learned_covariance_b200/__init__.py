@@ -19,10 +19,19 @@ Functions keep the C names:
     parallax_decode_ex(..., workspace) -> (y, lse)          caller-owned split scratch
     parallax_decode_paged(q, rho, kpages, vpages, block_table, seqlens) -> (y, lse)
                                                             paged cache, grouped query heads
+    parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp=, vexp=, ...) -> new_seqlens
+                                                            new tokens into a paged cache (e4m3 or bf16)
+    parallax_decode_paged_q8(q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc=None) -> (y, lse)
+                                                            decode over an e4m3 cache; adds attention weights to wacc
+    parallax_decode_paged_acc(q, rho, kpages, vpages, block_table, seqlens, wacc) -> (y, lse)
+                                                            the same over a bf16 cache
+    parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, budget, recent)
+        -> (new_seqlens, kept, new_wacc)                    keep the newest and most attended tokens
     parallax_rho_proj(x, W_R, H, d) -> rho
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -30,12 +39,13 @@ import threading
 __all__ = [
     "ParallaxError", "lib", "parallax_fwd", "parallax_fwd_fused", "parallax_fwd_train", "parallax_bwd",
     "parallax_decode", "parallax_softmax_decode", "parallax_decode_ex", "parallax_decode_paged",
+    "parallax_kv_append", "parallax_decode_paged_q8", "parallax_decode_paged_acc", "parallax_kv_evict",
     "parallax_rho_proj", "parallax_decode_workspace_bytes", "parallax_last_device_error",
-    "parallax_strerror", "parallax_device_sm_count", "LIB_PATH", "F32", "BF16",
+    "parallax_strerror", "parallax_device_sm_count", "LIB_PATH", "F32", "BF16", "E4M3",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libparallax.so")
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 _lock = threading.Lock()
 _lib = None
 
@@ -64,6 +74,10 @@ def lib() -> ctypes.CDLL:
             L.parallax_softmax_decode.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, P]
             L.parallax_decode_ex.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P, S, P]
             L.parallax_decode_paged.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P]
+            L.parallax_decode_paged_q8.argtypes = [P] * 11 + [I] * 9 + [P]
+            L.parallax_decode_paged_acc.argtypes = [P] * 9 + [I] * 9 + [P]
+            L.parallax_kv_append.argtypes = [P] * 13 + [I] * 9 + [P]
+            L.parallax_kv_evict.argtypes = [P] * 11 + [I] * 10 + [P]
             L.parallax_decode_workspace_bytes.argtypes = [I, I, I, I]
             L.parallax_decode_workspace_bytes.restype = S
             L.parallax_rho_proj.argtypes = [P, P, P, I, I, I, I, I, I, P]
@@ -73,7 +87,8 @@ def lib() -> ctypes.CDLL:
             L.parallax_device_sm_count.argtypes = []
             for f in (L.parallax_fwd, L.parallax_fwd_fused, L.parallax_fwd_train, L.parallax_bwd, L.parallax_decode,
                       L.parallax_softmax_decode, L.parallax_decode_ex, L.parallax_decode_paged,
-                      L.parallax_rho_proj,
+                      L.parallax_decode_paged_q8, L.parallax_decode_paged_acc, L.parallax_kv_append,
+                      L.parallax_kv_evict, L.parallax_rho_proj,
                       L.parallax_last_device_error, L.parallax_device_sm_count):
                 f.restype = I
             _lib = L
@@ -295,6 +310,191 @@ def parallax_decode_paged(q, rho, kpages, vpages, block_table, seqlens, out_dtyp
                                      num_pages, d, _dtype_code(q.dtype), _dtype_code(y.dtype), _stream(stream))
     _check(st, "parallax_decode_paged")
     return y, lse
+
+
+def _cache_dtype(kpages, kexp, vexp):
+    torch = _torch()
+    if kpages.dtype == torch.float8_e4m3fn:
+        if kexp is None or vexp is None:
+            raise ValueError("an e4m3 cache needs kexp and vexp")
+        return E4M3
+    if kpages.dtype == torch.bfloat16:
+        if kexp is not None or vexp is not None:
+            raise ValueError("a bf16 cache has no exponents")
+        return BF16
+    raise TypeError(f"unsupported cache dtype {kpages.dtype}")
+
+
+def _is(t, name, dtype, shape, device):
+    """A tensor a kernel reads or writes whole: contiguous, on `device`, of this dtype and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if not t.is_cuda or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+
+
+def _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens):
+    """Shapes of a paged cache; returns (B, Hkv, page_size, max_pages, num_pages, d, dtype code)."""
+    torch = _torch()
+    _need(kpages, "kpages")
+    if kpages.dim() != 4 or block_table.dim() != 2 or kpages.shape[2] < 16:
+        raise ValueError("kpages must be [num_pages, Hkv, page_size >= 16, d] and block_table [B, max_pages]")
+    dev, code = kpages.device, _cache_dtype(kpages, kexp, vexp)
+    num_pages, Hkv, page_size, d = kpages.shape
+    B, max_pages = block_table.shape
+    _is(vpages, "vpages", kpages.dtype, kpages.shape, dev)
+    if code == E4M3:
+        _is(kexp, "kexp", torch.int8, (num_pages, Hkv, page_size // 16), dev)
+        _is(vexp, "vexp", torch.int8, (num_pages, Hkv, page_size // 16), dev)
+    _is(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    _is(seqlens, "seqlens", torch.int32, (B,), dev)
+    return B, Hkv, page_size, max_pages, num_pages, d, code
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The tensors' device as the current one and `stream` (default: its current one) as its current
+    stream, so that outputs allocated inside belong to the stream that writes them."""
+    torch = _torch()
+    with contextlib.ExitStack() as es:
+        if device.index is not None and device.index != torch.cuda.current_device():
+            es.enter_context(torch.cuda.device(device))
+        if stream is not None:
+            es.enter_context(torch.cuda.stream(stream))
+        yield _stream(None)
+
+
+def parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp=None, vexp=None, counts=None,
+                       new_seqlens=None, wacc=None, stream=None):
+    """New tokens k, v [B, Hkv, T, d] bf16 behind each sequence's last; returns new_seqlens (int32 [B]).
+
+    k and v may be strided views with a dense last dimension (for instance a [B, T, Hkv, d]
+    projection transposed).  kpages, vpages: [num_pages, Hkv, page_size, d] bf16, or e4m3 with kexp,
+    vexp int8 [num_pages, Hkv, page_size / 16].  counts: int32 [B], tokens of each sequence (default
+    T).  wacc: the weight accumulator, whose entries of the new tokens become 0.
+    """
+    torch = _torch()
+    B, Hkv, ps, mp, npg, d, code = _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens)
+    dev = kpages.device
+    for t, n in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{n} must be bfloat16")
+        if t.device != dev or t.dim() != 4 or tuple(t.shape) != (B, Hkv, k.shape[2], d) or t.stride(3) != 1:
+            raise ValueError(f"{n} must be [B, Hkv, T, d] on {dev} with a dense last dimension")
+    T = k.shape[2]
+    if counts is not None:
+        _is(counts, "counts", torch.int32, (B,), dev)
+    if wacc is not None:
+        _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
+    strides = [(ctypes.c_longlong * 3)(*(s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape))) for t in (k, v)]
+    with _on(dev, stream) as st_:
+        if new_seqlens is None:
+            new_seqlens = torch.empty((B,), dtype=torch.int32, device=dev)
+        else:
+            _is(new_seqlens, "new_seqlens", torch.int32, (B,), dev)
+        st = lib().parallax_kv_append(_ptr(k), _ptr(v), ctypes.addressof(strides[0]), ctypes.addressof(strides[1]),
+                                      _ptr(kpages), _ptr(vpages), _ptr(kexp), _ptr(vexp), _ptr(block_table),
+                                      _ptr(seqlens), _ptr(counts), _ptr(new_seqlens), _ptr(wacc), B, Hkv, T, ps, mp,
+                                      npg, d, BF16, code, st_)
+    _check(st, "parallax_kv_append")
+    return new_seqlens
+
+
+def _decode_cache(name, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, out_dtype, y, lse, stream,
+                  want_lse):
+    torch = _torch()
+    B, Hkv, ps, mp, npg, d, code = _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens)
+    dev = kpages.device
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+        raise ValueError(f"q must be [B, Hq, d] = [{B}, Hq, {d}]")
+    Hq = q.shape[1]
+    _is(q, "q", torch.bfloat16, (B, Hq, d), dev)
+    if rho is not None:
+        _is(rho, "rho", torch.bfloat16, (B, Hq, d), dev)
+    if wacc is not None:
+        _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
+    with _on(dev, stream) as st_:
+        if y is None:
+            y = torch.empty((B, Hq, d), dtype=out_dtype or torch.float32, device=dev)
+        else:
+            _is(y, "y", y.dtype, (B, Hq, d), dev)
+        if lse is not None:
+            _is(lse, "lse", torch.float32, (B, Hq), dev)
+        elif want_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        sizes = (B, Hq, Hkv, ps, mp, npg, d, BF16, _dtype_code(y.dtype), st_)
+        if code == E4M3:
+            st = lib().parallax_decode_paged_q8(_ptr(q), _ptr(rho), _ptr(kpages), _ptr(vpages), _ptr(kexp),
+                                                _ptr(vexp), _ptr(block_table), _ptr(seqlens), _ptr(y), _ptr(lse),
+                                                _ptr(wacc), *sizes)
+        else:
+            st = lib().parallax_decode_paged_acc(_ptr(q), _ptr(rho), _ptr(kpages), _ptr(vpages), _ptr(block_table),
+                                                 _ptr(seqlens), _ptr(y), _ptr(lse), _ptr(wacc), *sizes)
+    _check(st, name)
+    return y, lse
+
+
+def parallax_decode_paged_q8(q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc=None, out_dtype=None,
+                             y=None, lse=None, stream=None, want_lse: bool = True):
+    """Decode over an e4m3 paged cache (value = code * 2^exp per block of 16 tokens and KV head).
+
+    q: [B, Hq, d] bf16; rho: the same, or None for softmax attention; kpages, vpages: [num_pages, Hkv,
+    page_size, d] float8_e4m3fn; kexp, vexp: int8 [num_pages, Hkv, page_size / 16]; wacc: None, or fp32
+    [B, Hkv, max_pages * page_size], to which the attention weight of each cached token, summed over
+    the query heads of its KV head, is added.
+    """
+    if kpages.dtype != _torch().float8_e4m3fn:
+        raise TypeError("kpages must be float8_e4m3fn")
+    return _decode_cache("parallax_decode_paged_q8", q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc,
+                         out_dtype, y, lse, stream, want_lse)
+
+
+def parallax_decode_paged_acc(q, rho, kpages, vpages, block_table, seqlens, wacc, out_dtype=None, y=None, lse=None,
+                              stream=None, want_lse: bool = True):
+    """parallax_decode_paged_q8 over a bf16 paged cache; wacc is required."""
+    if kpages.dtype != _torch().bfloat16:
+        raise TypeError("kpages must be bfloat16")
+    if wacc is None:
+        raise ValueError("wacc is required; without it use parallax_decode_paged")
+    return _decode_cache("parallax_decode_paged_acc", q, rho, kpages, vpages, None, None, block_table, seqlens, wacc,
+                         out_dtype, y, lse, stream, want_lse)
+
+
+def parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, budget: int, recent: int, kexp=None,
+                      vexp=None, new_seqlens=None, kept=None, new_wacc=None, stream=None):
+    """Keep min(L, budget) tokens per sequence and KV head: the newest `recent` and the heaviest others.
+
+    They move, in order, to the pages of new_table (int32 [B, new_max_pages], pages no entry of
+    block_table reaches).  Returns (new_seqlens int32 [B], kept int32 [B, Hkv, budget]: old positions,
+    new_wacc fp32 [B, Hkv, new_max_pages * page_size]); kept and new_wacc are written up to each
+    sequence's new length, and start as zero when they are allocated here.
+    """
+    torch = _torch()
+    B, Hkv, ps, mp, npg, d, code = _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens)
+    dev = kpages.device
+    _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
+    if new_table.dim() != 2:
+        raise ValueError("new_table must be [B, new_max_pages]")
+    nmp = new_table.shape[1]
+    _is(new_table, "new_table", torch.int32, (B, nmp), dev)
+    budget, recent = int(budget), int(recent)
+    if not 1 <= budget <= nmp * ps or not 0 <= recent <= budget:
+        raise ValueError("1 <= budget <= new_max_pages * page_size and 0 <= recent <= budget are wanted")
+    with _on(dev, stream) as st_:
+        if new_seqlens is None:
+            new_seqlens = torch.empty((B,), dtype=torch.int32, device=dev)
+        if kept is None:
+            kept = torch.zeros((B, Hkv, budget), dtype=torch.int32, device=dev)
+        if new_wacc is None:
+            new_wacc = torch.zeros((B, Hkv, nmp * ps), dtype=torch.float32, device=dev)
+        _is(new_seqlens, "new_seqlens", torch.int32, (B,), dev)
+        _is(kept, "kept", torch.int32, (B, Hkv, budget), dev)
+        _is(new_wacc, "new_wacc", torch.float32, (B, Hkv, nmp * ps), dev)
+        st = lib().parallax_kv_evict(_ptr(kpages), _ptr(vpages), _ptr(kexp), _ptr(vexp), _ptr(block_table),
+                                     _ptr(seqlens), _ptr(wacc), _ptr(new_table), _ptr(new_seqlens), _ptr(kept),
+                                     _ptr(new_wacc), B, Hkv, ps, mp, nmp, npg, d, budget, recent, code, st_)
+    _check(st, "parallax_kv_evict")
+    return new_seqlens, kept, new_wacc
 
 
 def parallax_rho_proj(x, W_R, H: int, d: int, rho=None, stream=None):

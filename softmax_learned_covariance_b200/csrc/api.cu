@@ -454,6 +454,135 @@ int parallax_decode_paged(const void *q, const void *rho, const void *kpages, co
                                          static_cast<float *>(ws), make_ctl(s), static_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// The paged layout shared by the cache calls: page_size -> shift, or a status.
+int paged_layout(const int *table, int B, int Hkv, int page_size, int max_pages, int num_pages, int d, PagedKV *pg) {
+    if (B < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1 || (d != 64 && d != 128)) return PARALLAX_ERR_SHAPE;
+    if (page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)) != 0) return PARALLAX_ERR_SHAPE;
+    int pshift = 0;
+    while ((1 << pshift) < page_size) ++pshift;
+    if ((long long)max_pages * page_size > (1ll << 30)) return PARALLAX_ERR_SHAPE;
+    if ((__int128)num_pages * Hkv * page_size * d > ((__int128)1 << 40)) return PARALLAX_ERR_SHAPE;
+    // per-token arrays and launch grids over (b, kvh, token)
+    if ((__int128)B * Hkv * max_pages * page_size > ((__int128)1 << 36)) return PARALLAX_ERR_SHAPE;
+    *pg = PagedKV{table, max_pages, num_pages, pshift, Hkv, 1};
+    return PARALLAX_OK;
+}
+
+// e4m3 caches have both exponent arrays, bf16 caches none.
+int cache_dtype_ok(int dtype, const void *kexp, const void *vexp) {
+    if (dtype == PARALLAX_E4M3) return kexp && vexp ? PARALLAX_OK : PARALLAX_ERR_NULL;
+    if (dtype == PARALLAX_BF16) return !kexp && !vexp ? PARALLAX_OK : PARALLAX_ERR_DTYPE;
+    return PARALLAX_ERR_DTYPE;
+}
+
+int decode_cache_impl(const void *q, const void *rho, const void *kpages, const void *vpages, const signed char *kexp,
+                      const signed char *vexp, const int *block_table, const int *seqlens, void *y, float *lse,
+                      float *wacc, int B, int Hq, int Hkv, int page_size, int max_pages, int num_pages, int d,
+                      int in_dtype, int out_dtype, parallax_stream_t stream) {
+    DecodeCacheArgs A{q, rho, kpages, vpages, kexp, vexp, {}, seqlens, y, lse, wacc, B, Hq, d, out_dtype};
+    int st = paged_layout(block_table, B, Hkv, page_size, max_pages, num_pages, d, &A.pg);
+    if (st) return st;
+    if (Hq < Hkv || Hq % Hkv != 0 || (long long)B * Hq > (1ll << 28)) return PARALLAX_ERR_SHAPE;
+    A.pg.group = Hq / Hkv;
+    if (!aligned16(q) || (rho && !aligned16(rho)) || !aligned16(kpages) || !aligned16(vpages) ||
+        !aligned4(block_table) || !aligned4(seqlens) || !aligned16(y) || (lse && !aligned4(lse)) ||
+        (wacc && !aligned16(wacc)))
+        return PARALLAX_ERR_ALIGN;
+    if (in_dtype != PARALLAX_BF16 || (out_dtype != PARALLAX_F32 && out_dtype != PARALLAX_BF16))
+        return PARALLAX_ERR_DTYPE;
+    DevState *s = nullptr;
+    if ((st = get_state(&s))) return st;
+    const DecodePlan plan = plan_decode_cache(B, Hq, Hkv, decode_cache_heads(rho != nullptr, A.pg.group),
+                                              max_pages * page_size, d, s->sms);
+    const DecodeCacheScratch need = decode_cache_scratch(A, plan);
+    void *ws = nullptr;
+    CallScratch scratch(s, static_cast<cudaStream_t>(stream));
+    if ((st = scratch.get(need.parts + need.hdr + need.zs, &ws))) return st;
+    return status_of(launch_decode_cache(A, plan, ws, make_ctl(s), static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int parallax_decode_paged_q8(const void *q, const void *rho, const void *kpages, const void *vpages,
+                             const signed char *kexp, const signed char *vexp, const int *block_table,
+                             const int *seqlens, void *y, float *lse, float *wacc, int B, int Hq, int Hkv,
+                             int page_size, int max_pages, int num_pages, int d, int in_dtype, int out_dtype,
+                             parallax_stream_t stream) {
+    if (!q || !kpages || !vpages || !kexp || !vexp || !block_table || !seqlens || !y) return PARALLAX_ERR_NULL;
+    return decode_cache_impl(q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, y, lse, wacc, B, Hq, Hkv,
+                             page_size, max_pages, num_pages, d, in_dtype, out_dtype, stream);
+}
+
+int parallax_decode_paged_acc(const void *q, const void *rho, const void *kpages, const void *vpages,
+                              const int *block_table, const int *seqlens, void *y, float *lse, float *wacc, int B,
+                              int Hq, int Hkv, int page_size, int max_pages, int num_pages, int d, int in_dtype,
+                              int out_dtype, parallax_stream_t stream) {
+    if (!q || !kpages || !vpages || !block_table || !seqlens || !y || !wacc) return PARALLAX_ERR_NULL;
+    return decode_cache_impl(q, rho, kpages, vpages, nullptr, nullptr, block_table, seqlens, y, lse, wacc, B, Hq, Hkv,
+                             page_size, max_pages, num_pages, d, in_dtype, out_dtype, stream);
+}
+
+int parallax_kv_append(const void *k, const void *v, const long long *k_strides, const long long *v_strides,
+                       void *kpages, void *vpages, signed char *kexp, signed char *vexp, const int *block_table,
+                       const int *seqlens, const int *counts, int *new_seqlens, float *wacc, int B, int Hkv, int T,
+                       int page_size, int max_pages, int num_pages, int d, int in_dtype, int cache_dtype,
+                       parallax_stream_t stream) {
+    if (!k || !v || !kpages || !vpages || !block_table || !seqlens) return PARALLAX_ERR_NULL;
+    KvAppendArgs A{k, v, {}, {}, kpages, vpages, kexp, vexp, {}, seqlens, counts, new_seqlens, wacc, B, T, d};
+    int st = paged_layout(block_table, B, Hkv, page_size, max_pages, num_pages, d, &A.pg);
+    if (st) return st;
+    if (T < 1 || T > (1 << 30) || (__int128)B * Hkv * T > ((__int128)1 << 34)) return PARALLAX_ERR_SHAPE;
+    if (in_dtype != PARALLAX_BF16) return PARALLAX_ERR_DTYPE;
+    if ((st = cache_dtype_ok(cache_dtype, kexp, vexp))) return st;
+    for (int i = 0; i < 3; ++i) {
+        const long long dense = i == 0 ? (long long)Hkv * T * d : (i == 1 ? (long long)T * d : d);
+        A.k_stride[i] = k_strides ? k_strides[i] : dense;
+        A.v_stride[i] = v_strides ? v_strides[i] : dense;
+        // rows are read in 16-byte pieces
+        if (A.k_stride[i] % 8 != 0 || A.v_stride[i] % 8 != 0) return PARALLAX_ERR_ALIGN;
+    }
+    if (!aligned16(k) || !aligned16(v) || !aligned16(kpages) || !aligned16(vpages) || !aligned4(block_table) ||
+        !aligned4(seqlens) || (counts && !aligned4(counts)) || (new_seqlens && !aligned4(new_seqlens)) ||
+        (wacc && !aligned16(wacc)))
+        return PARALLAX_ERR_ALIGN;
+    // other blocks of the launch still read the old lengths
+    if (new_seqlens && (new_seqlens == seqlens || new_seqlens == counts)) return PARALLAX_ERR_UNSUPPORTED;
+    DevState *s = nullptr;
+    if ((st = get_state(&s))) return st;
+    return status_of(launch_kv_append(A, make_ctl(s), static_cast<cudaStream_t>(stream)));
+}
+
+int parallax_kv_evict(void *kpages, void *vpages, signed char *kexp, signed char *vexp, const int *block_table,
+                      const int *seqlens, const float *wacc, const int *new_table, int *new_seqlens, int *kept,
+                      float *new_wacc, int B, int Hkv, int page_size, int max_pages, int new_max_pages, int num_pages,
+                      int d, int budget, int recent, int cache_dtype, parallax_stream_t stream) {
+    if (!kpages || !vpages || !block_table || !seqlens || !wacc || !new_table || !new_seqlens || !kept)
+        return PARALLAX_ERR_NULL;
+    KvEvictArgs A{kpages, vpages, kexp, vexp, {}, seqlens, wacc, new_table, new_seqlens, kept, new_wacc, B, d, budget,
+                  recent, new_max_pages};
+    int st = paged_layout(new_table, B, Hkv, page_size, new_max_pages, num_pages, d, &A.pg);
+    if (st) return st;
+    if ((st = paged_layout(block_table, B, Hkv, page_size, max_pages, num_pages, d, &A.pg))) return st;
+    if (budget < 1 || recent < 0 || recent > budget || budget > (long long)new_max_pages * page_size ||
+        (long long)B * Hkv > (1ll << 30))
+        return PARALLAX_ERR_SHAPE;
+    if ((st = cache_dtype_ok(cache_dtype, kexp, vexp))) return st;
+    if (!aligned16(kpages) || !aligned16(vpages) || !aligned4(block_table) || !aligned4(seqlens) || !aligned16(wacc) ||
+        !aligned4(new_table) || !aligned4(new_seqlens) || !aligned4(kept) || (new_wacc && !aligned16(new_wacc)))
+        return PARALLAX_ERR_ALIGN;
+    // the move reads what the source table names while it writes: nothing in place
+    if (new_table == block_table || new_seqlens == seqlens || new_wacc == wacc) return PARALLAX_ERR_UNSUPPORTED;
+    DevState *s = nullptr;
+    if ((st = get_state(&s))) return st;
+    return status_of(launch_kv_evict(A, make_ctl(s), static_cast<cudaStream_t>(stream)));
+}
+
 int parallax_decode_ex(const void *q, const void *rho, const void *kcache, const void *vcache, const int *seqlens,
                        void *y, float *lse, int B, int H, int Tcap, int d, int in_dtype, int out_dtype,
                        void *workspace, size_t workspace_bytes, parallax_stream_t stream) {

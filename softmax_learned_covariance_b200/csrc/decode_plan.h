@@ -51,4 +51,11 @@ inline DecodePlan plan_decode_paged(int B, int Hq, int Hkv, int Tcap, int d, int
     return plan_decode(B, Hkv * ((group + 7) / 8) * 4, Tcap, d, sm_count);
 }
 
+// The cache decode's units (decode_cache.cu) serve up to `heads` query heads of a
+// KV head and are sized like the paged decode's.
+inline DecodePlan plan_decode_cache(int B, int Hq, int Hkv, int heads, int Tcap, int d, int sm_count) {
+    const int group = Hq / Hkv;
+    return plan_decode(B, Hkv * ((group + heads - 1) / heads) * 4, Tcap, d, sm_count);
+}
+
 }  // namespace plx

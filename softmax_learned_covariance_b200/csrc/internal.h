@@ -65,6 +65,59 @@ cudaError_t launch_decode_paged(const void *q, const void *rho, const void *kpag
                                 int out_dtype, const DecodePlan &p, float *partials, const DeviceCtl &ctl,
                                 cudaStream_t s);
 
+// Paged decode over an e4m3 (kexp, vexp set) or bf16 cache, with or without a
+// probe (rho may be null), optionally adding attention weights to wacc
+// [B, Hkv, max_pages << pshift] (decode_cache.cu).
+struct DecodeCacheArgs {
+    const void *q, *rho, *kpages, *vpages;
+    const signed char *kexp, *vexp;
+    PagedKV pg;
+    const int *seqlens;
+    void *y;
+    float *lse, *wacc;
+    int B, Hq, d, out_dtype;
+};
+// Query heads one unit serves.
+int decode_cache_heads(bool with_rho, int group);
+// Scratch of a call in bytes, each part a multiple of 256: split partials, their
+// (m, l, abar) headers, and the scores that the accumulation reads back.
+struct DecodeCacheScratch {
+    size_t parts, hdr, zs;
+};
+DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, const DecodePlan &p);
+cudaError_t launch_decode_cache(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, const DeviceCtl &ctl,
+                                cudaStream_t s);
+
+// New tokens into a paged cache (kv_append.cu): k, v [B, Hkv, T, d] bf16 with
+// element strides (b, h, t); counts may be null (T each), as may new_seqlens and
+// wacc.
+struct KvAppendArgs {
+    const void *k, *v;
+    long long k_stride[3], v_stride[3];
+    void *kpages, *vpages;
+    signed char *kexp, *vexp;
+    PagedKV pg;
+    const int *seqlens, *counts;
+    int *new_seqlens;
+    float *wacc;
+    int B, T, d;
+};
+cudaError_t launch_kv_append(const KvAppendArgs &A, const DeviceCtl &ctl, cudaStream_t s);
+
+// Eviction by accumulated weight into the pages of new_table (kv_evict.cu).
+struct KvEvictArgs {
+    void *kpages, *vpages;
+    signed char *kexp, *vexp;
+    PagedKV pg;
+    const int *seqlens;
+    const float *wacc;
+    const int *new_table;
+    int *new_seqlens, *kept;
+    float *new_wacc;
+    int B, d, budget, recent, new_max_pages;
+};
+cudaError_t launch_kv_evict(const KvEvictArgs &A, const DeviceCtl &ctl, cudaStream_t s);
+
 // Wait policy and test hooks from the environment (PARALLAX_WAIT_TIMEOUT_MS,
 // PARALLAX_DEBUG_FLAGS) around the given device error word.  No allocation.
 DeviceCtl ctl_from_env(int *err);
