@@ -312,56 +312,62 @@ def parallax_decode_paged(q, rho, kpages, vpages, block_table, seqlens, out_dtyp
     return y, lse
 
 
-def _cache_dtype(kpages, kexp, vexp):
-    torch = _torch()
-    if kpages.dtype == torch.float8_e4m3fn:
-        if kexp is None or vexp is None:
-            raise ValueError("an e4m3 cache needs kexp and vexp")
-        return E4M3
-    if kpages.dtype == torch.bfloat16:
-        if kexp is not None or vexp is not None:
-            raise ValueError("a bf16 cache has no exponents")
-        return BF16
-    raise TypeError(f"unsupported cache dtype {kpages.dtype}")
-
-
 def _is(t, name, dtype, shape, device):
     """A tensor a kernel reads or writes whole: contiguous, on `device`, of this dtype and shape."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if not t.is_cuda or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
 
 
-def _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens):
-    """Shapes of a paged cache; returns (B, Hkv, page_size, max_pages, num_pages, d, dtype code)."""
-    torch = _torch()
+def _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens):
+    """Shapes of a paged cache; returns (device, B, Hkv, page_size, max_pages, num_pages, d, dtype code)."""
     _need(kpages, "kpages")
     if kpages.dim() != 4 or block_table.dim() != 2 or kpages.shape[2] < 16:
         raise ValueError("kpages must be [num_pages, Hkv, page_size >= 16, d] and block_table [B, max_pages]")
-    dev, code = kpages.device, _cache_dtype(kpages, kexp, vexp)
+    dev, dtype = kpages.device, kpages.dtype
     num_pages, Hkv, page_size, d = kpages.shape
     B, max_pages = block_table.shape
-    _is(vpages, "vpages", kpages.dtype, kpages.shape, dev)
-    if code == E4M3:
+    _is(vpages, "vpages", dtype, kpages.shape, dev)
+    if dtype == torch.float8_e4m3fn:
+        if kexp is None or vexp is None:
+            raise ValueError("an e4m3 cache needs kexp and vexp")
         _is(kexp, "kexp", torch.int8, (num_pages, Hkv, page_size // 16), dev)
         _is(vexp, "vexp", torch.int8, (num_pages, Hkv, page_size // 16), dev)
+        code = E4M3
+    elif dtype == torch.bfloat16:
+        if kexp is not None or vexp is not None:
+            raise ValueError("a bf16 cache has no exponents")
+        code = BF16
+    else:
+        raise TypeError(f"unsupported cache dtype {dtype}")
     _is(block_table, "block_table", torch.int32, (B, max_pages), dev)
     _is(seqlens, "seqlens", torch.int32, (B,), dev)
-    return B, Hkv, page_size, max_pages, num_pages, d, code
+    return dev, B, Hkv, page_size, max_pages, num_pages, d, code
+
+
+def _elsewhere(torch, device, stream):
+    """Whether a call has to change the current device or stream first (see _on)."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
 
 @contextlib.contextmanager
-def _on(device, stream):
+def _on(torch, device, stream):
     """The tensors' device as the current one and `stream` (default: its current one) as its current
     stream, so that outputs allocated inside belong to the stream that writes them."""
-    torch = _torch()
-    with contextlib.ExitStack() as es:
-        if device.index is not None and device.index != torch.cuda.current_device():
-            es.enter_context(torch.cuda.device(device))
-        if stream is not None:
-            es.enter_context(torch.cuda.stream(stream))
-        yield _stream(None)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream must be one of {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _raw_stream(torch, device):
+    # the handle of torch.cuda.current_stream(device) without building a Stream (0.1 against 2.2 us a call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp=None, vexp=None, counts=None,
@@ -374,28 +380,36 @@ def parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp=None, ve
     T).  wacc: the weight accumulator, whose entries of the new tokens become 0.
     """
     torch = _torch()
-    B, Hkv, ps, mp, npg, d, code = _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens)
-    dev = kpages.device
+    dev, B, Hkv, ps, mp, npg, d, code = _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens)
+    T = k.shape[2] if k.dim() == 4 else 0
+    strides = []
     for t, n in ((k, "k"), (v, "v")):
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{n} must be bfloat16")
-        if t.device != dev or t.dim() != 4 or tuple(t.shape) != (B, Hkv, k.shape[2], d) or t.stride(3) != 1:
-            raise ValueError(f"{n} must be [B, Hkv, T, d] on {dev} with a dense last dimension")
-    T = k.shape[2]
+        if t.shape != (B, Hkv, T, d) or t.device != dev:
+            raise ValueError(f"{n} must be [B, Hkv, T, d] = [{B}, {Hkv}, T, {d}] on {dev}")
+        if t.is_contiguous():
+            strides.append(None)
+            continue
+        sb, sh, st, si = t.stride()
+        if si != 1:
+            raise ValueError(f"{n} must have a dense last dimension")
+        # the stride of a dimension of size 1 means nothing
+        strides.append((ctypes.c_longlong * 3)(sb if B > 1 else 0, sh if Hkv > 1 else 0, st if T > 1 else 0))
     if counts is not None:
         _is(counts, "counts", torch.int32, (B,), dev)
     if wacc is not None:
         _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
-    strides = [(ctypes.c_longlong * 3)(*(s if n > 1 else 0 for s, n in zip(t.stride()[:3], t.shape))) for t in (k, v)]
-    with _on(dev, stream) as st_:
-        if new_seqlens is None:
-            new_seqlens = torch.empty((B,), dtype=torch.int32, device=dev)
-        else:
-            _is(new_seqlens, "new_seqlens", torch.int32, (B,), dev)
-        st = lib().parallax_kv_append(_ptr(k), _ptr(v), ctypes.addressof(strides[0]), ctypes.addressof(strides[1]),
-                                      _ptr(kpages), _ptr(vpages), _ptr(kexp), _ptr(vexp), _ptr(block_table),
-                                      _ptr(seqlens), _ptr(counts), _ptr(new_seqlens), _ptr(wacc), B, Hkv, T, ps, mp,
-                                      npg, d, BF16, code, st_)
+    if _elsewhere(torch, dev, stream):
+        with _on(torch, dev, stream):
+            return parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp, vexp, counts, new_seqlens, wacc)
+    if new_seqlens is None:
+        new_seqlens = torch.empty_like(seqlens)
+    else:
+        _is(new_seqlens, "new_seqlens", torch.int32, (B,), dev)
+    st = lib().parallax_kv_append(_at(k), _at(v), strides[0], strides[1], _at(kpages), _at(vpages), _at(kexp),
+                                  _at(vexp), _at(block_table), _at(seqlens), _at(counts), _at(new_seqlens), _at(wacc),
+                                  B, Hkv, T, ps, mp, npg, d, BF16, code, _raw_stream(torch, dev))
     _check(st, "parallax_kv_append")
     return new_seqlens
 
@@ -403,9 +417,8 @@ def parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp=None, ve
 def _decode_cache(name, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, out_dtype, y, lse, stream,
                   want_lse):
     torch = _torch()
-    B, Hkv, ps, mp, npg, d, code = _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens)
-    dev = kpages.device
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+    dev, B, Hkv, ps, mp, npg, d, code = _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens)
+    if q.dim() != 3:
         raise ValueError(f"q must be [B, Hq, d] = [{B}, Hq, {d}]")
     Hq = q.shape[1]
     _is(q, "q", torch.bfloat16, (B, Hq, d), dev)
@@ -413,23 +426,26 @@ def _decode_cache(name, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens
         _is(rho, "rho", torch.bfloat16, (B, Hq, d), dev)
     if wacc is not None:
         _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
-    with _on(dev, stream) as st_:
-        if y is None:
-            y = torch.empty((B, Hq, d), dtype=out_dtype or torch.float32, device=dev)
-        else:
-            _is(y, "y", y.dtype, (B, Hq, d), dev)
-        if lse is not None:
-            _is(lse, "lse", torch.float32, (B, Hq), dev)
-        elif want_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        sizes = (B, Hq, Hkv, ps, mp, npg, d, BF16, _dtype_code(y.dtype), st_)
-        if code == E4M3:
-            st = lib().parallax_decode_paged_q8(_ptr(q), _ptr(rho), _ptr(kpages), _ptr(vpages), _ptr(kexp),
-                                                _ptr(vexp), _ptr(block_table), _ptr(seqlens), _ptr(y), _ptr(lse),
-                                                _ptr(wacc), *sizes)
-        else:
-            st = lib().parallax_decode_paged_acc(_ptr(q), _ptr(rho), _ptr(kpages), _ptr(vpages), _ptr(block_table),
-                                                 _ptr(seqlens), _ptr(y), _ptr(lse), _ptr(wacc), *sizes)
+    if _elsewhere(torch, dev, stream):
+        with _on(torch, dev, stream):
+            return _decode_cache(name, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, out_dtype, y,
+                                 lse, None, want_lse)
+    if y is None:
+        y = torch.empty_like(q, dtype=out_dtype or torch.float32)
+    else:
+        _is(y, "y", y.dtype, (B, Hq, d), dev)
+    if lse is not None:
+        _is(lse, "lse", torch.float32, (B, Hq), dev)
+    elif want_lse:
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
+    if code == E4M3:
+        st = lib().parallax_decode_paged_q8(_at(q), _at(rho), _at(kpages), _at(vpages), _at(kexp), _at(vexp),
+                                            _at(block_table), _at(seqlens), _at(y), _at(lse), _at(wacc), B, Hq, Hkv,
+                                            ps, mp, npg, d, BF16, _dtype_code(y.dtype), _raw_stream(torch, dev))
+    else:
+        st = lib().parallax_decode_paged_acc(_at(q), _at(rho), _at(kpages), _at(vpages), _at(block_table),
+                                             _at(seqlens), _at(y), _at(lse), _at(wacc), B, Hq, Hkv, ps, mp, npg, d,
+                                             BF16, _dtype_code(y.dtype), _raw_stream(torch, dev))
     _check(st, name)
     return y, lse
 
@@ -470,8 +486,7 @@ def parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, bud
     sequence's new length, and start as zero when they are allocated here.
     """
     torch = _torch()
-    B, Hkv, ps, mp, npg, d, code = _check_cache(kpages, vpages, kexp, vexp, block_table, seqlens)
-    dev = kpages.device
+    dev, B, Hkv, ps, mp, npg, d, code = _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens)
     _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
     if new_table.dim() != 2:
         raise ValueError("new_table must be [B, new_max_pages]")
@@ -480,19 +495,25 @@ def parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, bud
     budget, recent = int(budget), int(recent)
     if not 1 <= budget <= nmp * ps or not 0 <= recent <= budget:
         raise ValueError("1 <= budget <= new_max_pages * page_size and 0 <= recent <= budget are wanted")
-    with _on(dev, stream) as st_:
-        if new_seqlens is None:
-            new_seqlens = torch.empty((B,), dtype=torch.int32, device=dev)
-        if kept is None:
-            kept = torch.zeros((B, Hkv, budget), dtype=torch.int32, device=dev)
-        if new_wacc is None:
-            new_wacc = torch.zeros((B, Hkv, nmp * ps), dtype=torch.float32, device=dev)
+    if _elsewhere(torch, dev, stream):
+        with _on(torch, dev, stream):
+            return parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, budget, recent, kexp, vexp,
+                                     new_seqlens, kept, new_wacc)
+    if new_seqlens is None:
+        new_seqlens = torch.empty_like(seqlens)
+    else:
         _is(new_seqlens, "new_seqlens", torch.int32, (B,), dev)
+    if kept is None:
+        kept = torch.zeros((B, Hkv, budget), dtype=torch.int32, device=dev)
+    else:
         _is(kept, "kept", torch.int32, (B, Hkv, budget), dev)
+    if new_wacc is None:
+        new_wacc = torch.zeros((B, Hkv, nmp * ps), dtype=torch.float32, device=dev)
+    else:
         _is(new_wacc, "new_wacc", torch.float32, (B, Hkv, nmp * ps), dev)
-        st = lib().parallax_kv_evict(_ptr(kpages), _ptr(vpages), _ptr(kexp), _ptr(vexp), _ptr(block_table),
-                                     _ptr(seqlens), _ptr(wacc), _ptr(new_table), _ptr(new_seqlens), _ptr(kept),
-                                     _ptr(new_wacc), B, Hkv, ps, mp, nmp, npg, d, budget, recent, code, st_)
+    st = lib().parallax_kv_evict(_at(kpages), _at(vpages), _at(kexp), _at(vexp), _at(block_table), _at(seqlens),
+                                 _at(wacc), _at(new_table), _at(new_seqlens), _at(kept), _at(new_wacc), B, Hkv, ps, mp,
+                                 nmp, npg, d, budget, recent, code, _raw_stream(torch, dev))
     _check(st, "parallax_kv_evict")
     return new_seqlens, kept, new_wacc
 
