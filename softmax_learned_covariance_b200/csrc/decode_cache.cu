@@ -16,12 +16,16 @@
 // a (token, head) in one thread, and one movmatrix per 8 tokens turns the
 // weights into the second product's operand.
 //
-// K and V go from global memory straight into MMA fragments: the order of the
-// contracted index is free as long as both operands agree, so a thread takes
-// the 16-byte chunks that a coalesced load gives it (K: chunks of its own two
-// tokens; V: the same chunk of its four tokens) as its part of the fragment.
-// No shared memory, barrier or ldmatrix is involved; the next tile's loads are
-// issued into the same registers as soon as a product has read them.
+// Each warp streams its own 16-token tiles through a ring in shared memory that
+// bulk copies (TMA) fill: K and V in four pieces of four tokens each, 32 bytes
+// apart from multiples of 128, which makes the threads' 16-byte reads free of
+// bank conflicts.  The order of the contracted index is free as long as both
+// operands agree, so a thread reads whole 16-byte chunks and uses them as its
+// part of the fragments (K: chunks of its own two tokens; V: the same chunk of
+// its four tokens): no ldmatrix and no barrier beyond the warp's own mbarriers.
+// The loads bound the kernel and how they are issued decides their rate (B=64,
+// 16 heads of their own, 4096 tokens, d = 128, 1.07 GB; loads alone): 16-byte
+// cp.async in fragment order 205 us, in row order 196 us, bulk copies 168 us.
 //
 // Numerics.  e4m3 codes are exact in fp16; q and rho are brought to fp16 by a
 // power of two per vector (exact down to 2^-22 of the vector's largest
@@ -32,12 +36,28 @@
 // far below the cache's own; l and abar sum the fp32 weights.
 #include <math.h>
 
+#include <type_traits>
+
 #include "cache_common.cuh"
+#include "sm100.cuh"
 
 namespace plx {
 namespace {
 
 constexpr int WARPS = 4;
+#ifndef Q8_STAGES
+#define Q8_STAGES 3
+#endif
+#ifndef BF_STAGES
+#define BF_STAGES 3
+#endif
+#ifndef MINB
+#define MINB 4
+#endif
+#ifndef UPS
+#define UPS 16
+#endif
+constexpr float MNONE = -1e30f;     // reference of a row that has seen no score
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 // A row's reference moves when a score exceeds it by 2^HEADROOM: p <= 2^4, and
@@ -51,16 +71,24 @@ __device__ __forceinline__ float fex2(float x) {
     return r;
 }
 
+// `bytes` (a multiple of 16) from global to shared memory; completion is counted on `bar`
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 template <bool Q8>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     if constexpr (Q8)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -69,7 +97,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // 8x8 matrix of 16-bit elements, one row per 4 threads -> its transpose
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
@@ -96,6 +124,11 @@ template <> __device__ __forceinline__ void store_y<__nv_bfloat16>(__nv_bfloat16
     *p = __float2bfloat16_rn(v);
 }
 
+constexpr int BAD = 1 << 16;     // a tile's page id is out of range
+
+// row in its piece of the x-th of a thread's four value tokens: columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
+__device__ __forceinline__ constexpr int x_row(int x) { return (x & 1) + 2 * (x >> 1); }
+
 // Shapes of one instantiation.  NT n-tiles of 8 vectors: 4 NT heads with a
 // probe, 8 NT without.
 template <int D, bool Q8, bool RHO, int NT> struct Shape {
@@ -109,26 +142,47 @@ template <int D, bool Q8, bool RHO, int NT> struct Shape {
     static constexpr int JS = D / 16;                    // MMAs of the value product
     // state of a warp in the merge: per head m, l, abar, then O[D] (and M[D])
     static constexpr int MSTRIDE = (RHO ? 2 : 1) * D + 4;
-    static constexpr int MERGE_FLOATS = WARPS * HEADS * MSTRIDE;
+    static constexpr int MERGE_BYTES = WARPS * HEADS * MSTRIDE * 4;
+    // K or V of 16 tokens: four pieces of four rows, 32 bytes off a multiple of 128
+    static constexpr int PIECE = 4 * ROW + 32;
+    static constexpr int TILE_BYTES = 2 * 4 * PIECE;
+    // Token of a thread's score rows r = 2 m + o and r + 8: row o (and o + 2) of piece m,
+    // or, for the odd rows of 128-byte and wider rows, of the piece 64 bytes further in
+    // the banks; so the 8 threads of a shared-memory phase read 8 different chunks.
+    static constexpr int ODD_PIECE = ROW == 64 ? 0 : 2;
+    static constexpr int STAGES = Q8 ? Q8_STAGES : BF_STAGES;            // tiles in flight per warp: STAGES - 1
+    static constexpr int RING_BYTES = WARPS * STAGES * TILE_BYTES;
+    static constexpr int SMEM = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
 };
 
 // Partials of a split unit: O[D] (and M[D]) per (b, h, split); its m, l, abar in `hdr`.
 template <int D, bool RHO> constexpr int part_stride() { return (RHO ? 2 : 1) * D; }
 
 template <int D, bool Q8, bool RHO, int NT, typename Tout>
-__global__ void __launch_bounds__(WARPS * 32) k_decode_cache(
+__global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cache(
     const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ rho, const uint8_t *__restrict__ kp,
     const uint8_t *__restrict__ vp, const signed char *__restrict__ kexp, const signed char *__restrict__ vexp,
     const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse, int Hq, int chunk, int nsplit,
     long units_per_split, int htiles, PagedKV pg, float *__restrict__ parts, float4 *__restrict__ hdr,
-    float *__restrict__ zs, int *__restrict__ err) {
+    float *__restrict__ zs, DeviceCtl ctl) {
     using S = Shape<D, Q8, RHO, NT>;
-    __shared__ __align__(16) float merge[S::MERGE_FLOATS];
+    extern __shared__ __align__(128) uint8_t smem[];
+    float *merge = reinterpret_cast<float *>(smem);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r = lane / 4, t4 = lane % 4;
     const float scale_log2 = LOG2E / sqrtf((float)D);
     const int ps = 1 << pg.pshift, pmask = ps - 1;
     const long units = units_per_split * nsplit;
+    __shared__ uint64_t full[WARPS][S::STAGES];
+    __shared__ int abort_flag;
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (lane == 0)
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+    fence_mbar_init();
+    __syncthreads();
+    const WaitCtl wait{ctl.err, &abort_flag, ctl.wait_ns};
+    int stage = 0;               // stage of this warp's next tile
+    uint32_t phases = 0;         // parity each stage's barrier completes next
 
     for (long u = blockIdx.x; u < units; u += gridDim.x) {
         const long ut = u % units_per_split;    // chunk-major
@@ -205,155 +259,192 @@ __global__ void __launch_bounds__(WARPS * 32) k_decode_cache(
         float mref[S::HPT], lsum[S::HPT], asum[S::HPT];
 #pragma unroll
         for (int i = 0; i < S::HPT; ++i) {
-            mref[i] = -INFINITY;
+            mref[i] = MNONE;
             lsum[i] = asum[i] = 0.f;
         }
-        float evref = -1000.f;    // exponent O and M are held at (e4m3)
+        int evref = -1000;        // exponent O and M are held at (e4m3)
 
-        auto page_of = [&](int i) -> int {
-            return pg.table[(size_t)b * pg.max_pages + ((t0 + i * 16) >> pg.pshift)];
+        // This warp's tiles are warp + WARPS j.  Lane l holds the page of tile 32 n + l
+        // (a tile's rows share one page: it starts on a multiple of 16 and pages hold at
+        // least 16) and its two exponents, loaded 32 tiles at a time.
+        const int mine = ntiles > warp ? (ntiles - warp + WARPS - 1) / WARPS : 0;
+        auto page_of = [&](int j) -> int {
+            return j < mine ? pg.table[(size_t)b * pg.max_pages + ((t0 + (warp + WARPS * j) * 16) >> pg.pshift)] : 0;
         };
-        uint4 kr[2][S::KC];              // rows r and r + 8 of the tile
-        uint32_t vr[4][S::VB / 4];       // rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
-        int ke = 0, ve = 0, kid = 0, vid = 0;
-        // a tile's rows share one page: it starts on a multiple of 16, pages hold at least 16
-        auto load_k = [&](int i, int id) {
-            const int t = t0 + i * 16;
-            const bool ok = (unsigned)id < (unsigned)pg.num_pages;
-            if (!ok && lane == 0) atomicExch(err, PARALLAX_ERR_DEVICE_INDEX);
-            const size_t slab = (size_t)(ok ? id : 0) * pg.Hkv + kvh;
-            const uint8_t *base = kp + (slab * ps + (t & pmask)) * S::ROW + 16 * t4;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int c = 0; c < S::KC; ++c)
-                    kr[x][c] = ok && t + r + 8 * x < t1 ? ldg_nc16(base + (r + 8 * x) * S::ROW + 64 * c)
-                                                        : make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (Q8) ke = ok ? kexp[slab * (ps / KV_BLOCK) + (t & pmask) / KV_BLOCK] : 0;
-        };
-        auto load_v = [&](int i, int id) {
-            const int t = t0 + i * 16;
-            const bool ok = (unsigned)id < (unsigned)pg.num_pages;
-            const size_t slab = (size_t)(ok ? id : 0) * pg.Hkv + kvh;
-            const uint8_t *base = vp + (slab * ps + (t & pmask)) * S::ROW + (S::VB < 16 ? S::VB : 16) * r;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int row = 2 * t4 + (x & 1) + 8 * (x >> 1);
-                const bool in = ok && t + row < t1;
-                if constexpr (S::VB == 8) {
-                    const uint2 v = in ? ldg_nc8(base + row * S::ROW) : make_uint2(0u, 0u);
-                    vr[x][0] = v.x;
-                    vr[x][1] = v.y;
-                } else {
-#pragma unroll
-                    for (int c = 0; c < S::VB / 16; ++c) {
-                        const uint4 v = in ? ldg_nc16(base + row * S::ROW + 128 * c) : make_uint4(0u, 0u, 0u, 0u);
-                        vr[x][4 * c] = v.x;
-                        vr[x][4 * c + 1] = v.y;
-                        vr[x][4 * c + 2] = v.z;
-                        vr[x][4 * c + 3] = v.w;
-                    }
-                }
+        // exponents of K (low byte) and V (next byte), and BAD for a page id out of range
+        auto info_of = [&](int j, int id) -> int {
+            if (j >= mine) return 0;
+            if ((unsigned)id >= (unsigned)pg.num_pages) {
+                atomicExch(ctl.err, PARALLAX_ERR_DEVICE_INDEX);
+                return BAD;
             }
-            if constexpr (Q8) ve = ok ? vexp[slab * (ps / KV_BLOCK) + (t & pmask) / KV_BLOCK] : 0;
+            if constexpr (!Q8) return 0;
+            const size_t at = ((size_t)id * pg.Hkv + kvh) * (ps / KV_BLOCK) +
+                              ((t0 + (warp + WARPS * j) * 16) & pmask) / KV_BLOCK;
+            return (kexp[at] & 0xff) | (vexp[at] & 0xff) << 8;
         };
+        int ids = page_of(lane), ids_next = 0, info = info_of(lane, ids), info_next = 0;
 
-        // this warp's tiles: warp, warp + WARPS, ...
-        if (warp < ntiles) {
-            kid = page_of(warp);
-            load_k(warp, kid);
-            load_v(warp, kid);
-            if (warp + WARPS < ntiles) vid = page_of(warp + WARPS);
+        uint8_t *ring = smem + warp * S::STAGES * S::TILE_BYTES;
+        // copies tile j from page `id` into stage st, lane l < 8 one piece of K (l < 4) or V;
+        // rows past t1, and all rows of a bad page, are left out
+        auto issue = [&](int j, int st, int id) {
+            const int t = t0 + (warp + WARPS * j) * 16;
+            const bool ok = (unsigned)id < (unsigned)pg.num_pages;
+            const int rows = ok ? min(16, t1 - t) : 0;
+            const uint32_t bar = smem_u32(&full[warp][st]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * rows * S::ROW);
+            __syncwarp();
+            const int piece = lane & 3, n = min(rows - 4 * piece, 4);
+            const bool skip = (ctl.debug_flags & DEBUG_DECODE_SKIP_FIRST_TILE) != 0 && j == 0;
+            if (lane < 8 && n > 0 && !skip) {
+                const size_t row = (((size_t)id * pg.Hkv + kvh) << pg.pshift) + (t & pmask) + 4 * piece;
+                bulk_load(smem_u32(ring + st * S::TILE_BYTES + lane * S::PIECE), (lane < 4 ? kp : vp) + row * S::ROW,
+                          n * S::ROW, bar);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < S::STAGES - 1; ++j) {
+            const int id = __shfl_sync(0xffffffffu, ids, j);
+            if (j < mine) issue(j, (stage + j) % S::STAGES, id);
         }
-        for (int i = warp; i < ntiles; i += WARPS) {
-            const int next = i + WARPS;
-            const bool more = next < ntiles;
-            // ---- scores ----
-            float sc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-#pragma unroll
-            for (int s = 0; s < S::KSTEPS; ++s) {
-                uint32_t a0, a1, a2, a3;
-                if constexpr (Q8) {
-                    e4m3x4_to_f16x2((&kr[0][s / 4].x)[s % 4], a0, a2);
-                    e4m3x4_to_f16x2((&kr[1][s / 4].x)[s % 4], a1, a3);
-                } else {
-                    const int c = s / 2, w = 2 * (s % 2);
-                    a0 = (&kr[0][c].x)[w];
-                    a2 = (&kr[0][c].x)[w + 1];
-                    a1 = (&kr[1][c].x)[w];
-                    a3 = (&kr[1][c].x)[w + 1];
+        // where this thread's tokens and chunks lie in a tile
+        const int tok0 = 4 * ((r / 2 + (r & 1) * S::ODD_PIECE) & 3) + (r & 1), tok1 = tok0 + 2;
+        const uint32_t koff = (tok0 / 4) * S::PIECE + (tok0 & 3) * S::ROW + 16 * t4;
+        const int vpiece[2] = {t4, (t4 + S::ODD_PIECE) & 3};
+        const uint32_t voff = (S::VB < 16 ? S::VB : 16) * r;
+        for (int j = 0; j < mine; ++j) {
+            // ---- pages and exponents of the 32 tiles after these, in good time ----
+            if ((j & 31) == 0)
+                ids_next = page_of(j + 32 + lane);
+            else if ((j & 31) == 16)
+                info_next = info_of(j + 16 + lane, ids_next);
+            const int jn = j + S::STAGES - 1;
+            const int id = __shfl_sync(0xffffffffu, (j & 31) + S::STAGES - 1 < 32 ? ids : ids_next, jn & 31);
+            // every lane has read the tile before this one: its stage takes tile jn
+            if (jn < mine) issue(jn, stage == 0 ? S::STAGES - 1 : stage - 1, id);
+            const int now = __shfl_sync(0xffffffffu, info, j & 31);
+            const int ke = (int)(signed char)now, ve = (int)(signed char)(now >> 8);
+            if ((j & 31) == 31) {
+                ids = ids_next;
+                info = info_next;
+            }
+            const bool landed = mbar_wait(smem_u32(&full[warp][stage]), (phases >> stage) & 1u, wait);
+            if (!__all_sync(0xffffffffu, landed)) {
+                // give up: let this warp's copies land (bounded) before the CTA's memory goes
+                for (int i = j; i < min(jn + 1, mine); ++i) {
+                    const int st = (stage + i - j) % S::STAGES;
+                    mbar_wait_drain(smem_u32(&full[warp][st]), (phases >> st) & 1u, 2000000ull);
                 }
+                break;
+            }
+            phases ^= 1u << stage;
+            const uint8_t *dk = ring + stage * S::TILE_BYTES, *dv = dk + 4 * S::PIECE;
+            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
+            const int tile = t0 + (warp + WARPS * j) * 16;
+            const int nvalid = t1 - tile;                   // tokens of the tile
+            const int nread = now & BAD ? 0 : nvalid;       // rows of it that were copied
+
+            // ---- scores ----
+            float sc[NT][4], sc2[NT][4];          // two chains of products
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816<Q8>(sc[nt], a0, a1, a2, a3, qf[nt][s][0], qf[nt][s][1]);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][e] = sc2[nt][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < S::KC; ++c) {
+                uint4 k0 = *reinterpret_cast<const uint4 *>(dk + koff + 64 * c);
+                uint4 k1 = *reinterpret_cast<const uint4 *>(dk + koff + 2 * S::ROW + 64 * c);
+                if (nread < 16) {                           // what was not copied is not looked at
+                    if (tok0 >= nread) k0 = make_uint4(0u, 0u, 0u, 0u);
+                    if (tok1 >= nread) k1 = make_uint4(0u, 0u, 0u, 0u);
+                }
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                for (int i = 0; i < (Q8 ? 4 : 2); ++i) {
+                    const int st = c * (Q8 ? 4 : 2) + i;
+                    uint32_t a0, a1, a2, a3;
+                    if constexpr (Q8) {
+                        e4m3x4_to_f16x2(w0[i], a0, a2);
+                        e4m3x4_to_f16x2(w1[i], a1, a3);
+                    } else {
+                        a0 = w0[2 * i];
+                        a2 = w0[2 * i + 1];
+                        a1 = w1[2 * i];
+                        a3 = w1[2 * i + 1];
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<Q8>(st % 2 ? sc2[nt] : sc[nt], a0, a1, a2, a3, qf[nt][st][0], qf[nt][st][1]);
+                }
             }
-            const float kscale = Q8 ? exp2_whole(ke) : 1.f;
-            const float evt = (float)ve;
-            const int id = vid;                                     // page of the next tile
-            if (more) {
-                load_k(next, id);
-                if (next + WARPS < ntiles) vid = page_of(next + WARPS);
-            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][e] += sc2[nt][e];
 
             // ---- weights ----
-            const int nvalid = t1 - (t0 + i * 16);
-            const bool in0 = r < nvalid, in1 = r + 8 < nvalid;
-            float z[S::HPT][2], a[S::HPT][2];
-            bool up = Q8 && evt > evref;
+            float f[S::HPT], dz[S::HPT][2];       // score = sc * f; dz: against the reference
+            bool up = Q8 && ve > evref;
+            const float kscale = Q8 ? exp2_whole(ke) : 1.f;
 #pragma unroll
             for (int h = 0; h < S::HPT; ++h) {
                 const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
-                // two products: the factors' own product could overflow where a score is 0
-                z[h][0] = in0 ? sc[nt][e] * zfac[h] * kscale : -INFINITY;
-                z[h][1] = in1 ? sc[nt][2 + e] * zfac[h] * kscale : -INFINITY;
-                if constexpr (RHO) {
-                    a[h][0] = sc[nt][1] * afac[h] * kscale;
-                    a[h][1] = sc[nt][3] * afac[h] * kscale;
+                f[h] = Q8 ? fminf(zfac[h] * kscale, 3e38f) : zfac[h];     // finite: a score of 0 stays 0
+                dz[h][0] = fmaf(sc[nt][e], f[h], -mref[h]);
+                dz[h][1] = fmaf(sc[nt][2 + e], f[h], -mref[h]);
+                if (nvalid < 16) {
+                    if (tok0 >= nvalid) dz[h][0] = -INFINITY;
+                    if (tok1 >= nvalid) dz[h][1] = -INFINITY;
                 }
-                up |= fmaxf(z[h][0], z[h][1]) > mref[h] + HEADROOM;
+                up |= fmaxf(dz[h][0], dz[h][1]) > HEADROOM;
             }
             if (zs != nullptr) {
-                float *dst = zs + ((((size_t)b * pg.Hkv + kvh) * htiles + ht) * (size_t)Tcap + t0 + i * 16) * S::HEADS;
+                float *dst = zs + ((((size_t)b * pg.Hkv + kvh) * htiles + ht) * (size_t)Tcap + tile) * S::HEADS;
 #pragma unroll
                 for (int h = 0; h < S::HPT; ++h) {
+                    const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
                     const int head = RHO ? 4 * h + t4 : 8 * (h / 2) + 2 * t4 + h % 2;
-                    if (in0) dst[r * S::HEADS + head] = z[h][0];
-                    if (in1) dst[(r + 8) * S::HEADS + head] = z[h][1];
+                    if (tok0 < nvalid) dst[tok0 * S::HEADS + head] = sc[nt][e] * f[h];
+                    if (tok1 < nvalid) dst[tok1 * S::HEADS + head] = sc[nt][2 + e] * f[h];
                 }
             }
             if (__any_sync(0xffffffffu, up)) {
-                const float evnew = fmaxf(evref, evt);
-                const float vshift = Q8 ? fex2(evref - evnew) : 1.f;
-                evref = evnew;
+                const float vshift = Q8 ? fex2((float)min(evref - ve, 0)) : 1.f;
+                evref = max(evref, ve);
 #pragma unroll
                 for (int h = 0; h < S::HPT; ++h) {
-                    float mx = fmaxf(z[h][0], z[h][1]);
+                    const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
+                    float z0 = sc[nt][e] * f[h], z1 = sc[nt][2 + e] * f[h];
+                    if (tok0 >= nvalid) z0 = -INFINITY;
+                    if (tok1 >= nvalid) z1 = -INFINITY;
+                    float mx = fmaxf(z0, z1);
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                     const float mnew = fmaxf(mref[h], mx);
-                    const float alpha = mref[h] == -INFINITY ? 0.f : fex2(mref[h] - mnew);
+                    const float alpha = fex2(mref[h] - mnew);
                     mref[h] = mnew;
+                    dz[h][0] = z0 - mnew;
+                    dz[h][1] = z1 - mnew;
                     lsum[h] *= alpha;
                     asum[h] *= alpha;
                     const float beta = alpha * vshift;
-                    const int nt = RHO ? h : h / 2;
 #pragma unroll
-                    for (int j = 0; j < S::JS; ++j) {
+                    for (int i = 0; i < S::JS; ++i) {
                         if constexpr (RHO) {
-                            oacc[nt][j][0] *= beta;
-                            oacc[nt][j][1] *= beta;
-                            oacc[nt][j][2] *= beta;
-                            oacc[nt][j][3] *= beta;
+                            oacc[nt][i][0] *= beta;
+                            oacc[nt][i][1] *= beta;
+                            oacc[nt][i][2] *= beta;
+                            oacc[nt][i][3] *= beta;
                         } else {
-                            oacc[nt][j][h % 2] *= beta;
-                            oacc[nt][j][2 + h % 2] *= beta;
+                            oacc[nt][i][e] *= beta;
+                            oacc[nt][i][2 + e] *= beta;
                         }
                     }
                 }
             }
-            const float vfac = Q8 ? fex2(evt - evref) : 1.f;
+            const float vfac = Q8 ? fex2((float)(ve - evref)) : 1.f;
             uint32_t bh[NT][2], bl[NT][2];    // weights as the value product's operand: hi, lo parts
 #pragma unroll
             for (int x = 0; x < 2; ++x)
@@ -361,15 +452,16 @@ __global__ void __launch_bounds__(WARPS * 32) k_decode_cache(
                 for (int nt = 0; nt < NT; ++nt) {
                     float w0, w1;
                     if constexpr (RHO) {
-                        // masked tokens have z = -inf and a = 0
-                        const float p = fex2(z[nt][x] - (mref[nt] == -INFINITY ? 0.f : mref[nt]));
+                        // masked tokens have p = 0 and, their K rows being zero, a = 0
+                        const float p = fex2(dz[nt][x]);
+                        const float a = sc[nt][2 * x + 1] * (Q8 ? fminf(afac[nt] * kscale, 3e38f) : afac[nt]);
                         lsum[nt] += p;
-                        asum[nt] = fmaf(p, a[nt][x], asum[nt]);
+                        asum[nt] = fmaf(p, a, asum[nt]);
                         w0 = p * vfac;
-                        w1 = w0 * (a[nt][x] * (1.f / ASCALE));
+                        w1 = w0 * (a * (1.f / ASCALE));
                     } else {
-                        w0 = fex2(z[2 * nt][x] - (mref[2 * nt] == -INFINITY ? 0.f : mref[2 * nt]));
-                        w1 = fex2(z[2 * nt + 1][x] - (mref[2 * nt + 1] == -INFINITY ? 0.f : mref[2 * nt + 1]));
+                        w0 = fex2(dz[2 * nt][x]);
+                        w1 = fex2(dz[2 * nt + 1][x]);
                         lsum[2 * nt] += w0;
                         lsum[2 * nt + 1] += w1;
                         w0 *= vfac;
@@ -382,29 +474,58 @@ __global__ void __launch_bounds__(WARPS * 32) k_decode_cache(
                 }
             // ---- O += P V, M += (P o A) V ----
 #pragma unroll
-            for (int j = 0; j < S::JS; ++j) {
-                uint32_t a0, a1, a2, a3;
-                if constexpr (Q8) {
-                    const uint32_t sel = j % 2 ? 0x7362u : 0x5140u;   // two elements of both tokens, element-major
-                    e4m3x4_to_f16x2(__byte_perm(vr[0][j / 2], vr[1][j / 2], sel), a0, a1);
-                    e4m3x4_to_f16x2(__byte_perm(vr[2][j / 2], vr[3][j / 2], sel), a2, a3);
-                } else {
-                    a0 = __byte_perm(vr[0][j], vr[1][j], 0x5410);
-                    a1 = __byte_perm(vr[0][j], vr[1][j], 0x7632);
-                    a2 = __byte_perm(vr[2][j], vr[3][j], 0x5410);
-                    a3 = __byte_perm(vr[2][j], vr[3][j], 0x7632);
-                }
+            for (int c = 0; c < (S::VB + 15) / 16; ++c) {
+                uint32_t v[4][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma16816<Q8>(oacc[nt][j], a0, a1, a2, a3, bh[nt][0], bh[nt][1]);
-                    mma16816<Q8>(oacc[nt][j], a0, a1, a2, a3, bl[nt][0], bl[nt][1]);
+                for (int x = 0; x < 4; ++x) {       // tokens of the weights' columns 2 t4, 2 t4 + 1, + 8, + 9
+                    const uint8_t *src = dv + vpiece[x & 1] * S::PIECE + x_row(x) * S::ROW + voff + 128 * c;
+                    if constexpr (S::VB < 16) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                        v[x][0] = w.x;
+                        v[x][1] = w.y;
+                    } else {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src);
+                        v[x][0] = w.x;
+                        v[x][1] = w.y;
+                        v[x][2] = w.z;
+                        v[x][3] = w.w;
+                    }
+                    if (nread < 16 && 4 * vpiece[x & 1] + x_row(x) >= nread) v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0u;
+                }
+                constexpr int PER = S::JS / ((S::VB + 15) / 16);      // MMAs of a chunk
+#pragma unroll
+                for (int g = 0; g < PER; g += 4) {                   // hi parts of four, then their lo parts
+                    uint32_t av[4][4];
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const int i = g + q4;
+                        if constexpr (Q8) {
+                            const uint32_t sel = i % 2 ? 0x7362u : 0x5140u;   // two elements of both tokens, element-major
+                            e4m3x4_to_f16x2(__byte_perm(v[0][i / 2], v[1][i / 2], sel), av[q4][0], av[q4][1]);
+                            e4m3x4_to_f16x2(__byte_perm(v[2][i / 2], v[3][i / 2], sel), av[q4][2], av[q4][3]);
+                        } else {
+                            av[q4][0] = __byte_perm(v[0][i], v[1][i], 0x5410);
+                            av[q4][1] = __byte_perm(v[0][i], v[1][i], 0x7632);
+                            av[q4][2] = __byte_perm(v[2][i], v[3][i], 0x5410);
+                            av[q4][3] = __byte_perm(v[2][i], v[3][i], 0x7632);
+                        }
+                    }
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<Q8>(oacc[nt][c * PER + g + q4], av[q4][0], av[q4][1], av[q4][2], av[q4][3],
+                                             part ? bl[nt][0] : bh[nt][0], part ? bl[nt][1] : bh[nt][1]);
                 }
             }
-            if (more) load_v(next, id);
         }
+        __syncthreads();   // every warp is done with its ring: reuse it for the merge
+        if (abort_flag) return;
 
         // ---- merge the warps' states per head ----
-        const float oscale = Q8 ? exp2_whole((int)evref) : 1.f;
+        const float oscale = Q8 ? exp2_whole(evref) : 1.f;
         float *mg = merge + warp * S::HEADS * S::MSTRIDE;
 #pragma unroll
         for (int h = 0; h < S::HPT; ++h) {
@@ -440,15 +561,14 @@ __global__ void __launch_bounds__(WARPS * 32) k_decode_cache(
         __syncthreads();
         for (int idx = threadIdx.x; idx < nh * D; idx += WARPS * 32) {
             const int hh = idx / D, e = idx % D;
-            float mu = -INFINITY;
+            float mu = MNONE;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) mu = fmaxf(mu, merge[(w * S::HEADS + hh) * S::MSTRIDE]);
             float l = 0.f, ab = 0.f, o = 0.f, m = 0.f;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
                 const float *src = merge + (w * S::HEADS + hh) * S::MSTRIDE;
-                // a warp without a tile has m = -inf (its sums are 0); scores that are all -inf weigh 1
-                const float f = src[0] == mu ? 1.f : fex2(src[0] - mu);
+                const float f = fex2(src[0] - mu);    // 0 for a warp without a tile
                 l = fmaf(f, src[1], l);
                 o = fmaf(f, src[4 + e], o);
                 if constexpr (RHO) {
@@ -473,7 +593,8 @@ __global__ void __launch_bounds__(WARPS * 32) k_decode_cache(
             }
             if (e == 0 && hdr != nullptr) hdr[bh * nsplit + split] = make_float4(mu, l, ab, 0.f);
         }
-        __syncthreads();   // the merge area is the next unit's
+        fence_proxy_async();   // the next unit's copies write where these stores and loads went
+        __syncthreads();
     }
 }
 
@@ -523,7 +644,7 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
         for (int s = grp; s < nv; s += GROUPS) {
             const float4 h = H[s];
             const float4 p = P[(size_t)s * COLS];
-            const float w = h.x == mu ? 1.f : fex2(h.x - mu);
+            const float w = fex2(h.x - mu);
             l = fmaf(w, h.y, l);
             ab = fmaf(w, h.z, ab);
             acc.x = fmaf(w, p.x, acc.x);
@@ -578,7 +699,7 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
             for (int s = lane; s < nv; s += 32) mu = fmaxf(mu, H[s].x);
 #pragma unroll
             for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
-            for (int s = lane; s < nv; s += 32) l += (H[s].x == mu ? 1.f : fex2(H[s].x - mu)) * H[s].y;
+            for (int s = lane; s < nv; s += 32) l += fex2(H[s].x - mu) * H[s].y;
 #pragma unroll
             for (int off = 16; off > 0; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
             if (lane == 0) slse[h] = mu + log2f(l);
@@ -612,7 +733,7 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
 template <bool RHO> int heads_for(int group) { return RHO ? (group <= 4 ? 4 : 8) : 8; }
 
 template <int D, bool Q8, bool RHO, int NT, typename Tout>
-cudaError_t launch_t(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, int *err, cudaStream_t s) {
+cudaError_t launch_t(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, const DeviceCtl &ctl, cudaStream_t s) {
     using S = Shape<D, Q8, RHO, NT>;
     const int htiles = (A.pg.group + S::HEADS - 1) / S::HEADS;
     const int Tcap = A.pg.max_pages << A.pg.pshift;
@@ -624,10 +745,12 @@ cudaError_t launch_t(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, in
     float *zs = sc.zs ? reinterpret_cast<float *>(base + sc.parts + sc.hdr) : nullptr;
     const long per_split = (long)A.B * A.pg.Hkv * htiles;
     const long units = per_split * p.nsplit;
-    k_decode_cache<D, Q8, RHO, NT, Tout><<<(unsigned)(units < 0x7fffffffL ? units : 0x7fffffffL), WARPS * 32, 0, s>>>(
+    static std::atomic<unsigned long long> limit_set{0};
+    if (cudaError_t e = ensure_smem_limit(k_decode_cache<D, Q8, RHO, NT, Tout>, S::SMEM, limit_set)) return e;
+    k_decode_cache<D, Q8, RHO, NT, Tout><<<(unsigned)(units < 0x7fffffffL ? units : 0x7fffffffL), WARPS * 32, S::SMEM, s>>>(
         (const __nv_bfloat16 *)A.q, (const __nv_bfloat16 *)A.rho, (const uint8_t *)A.kpages, (const uint8_t *)A.vpages,
         A.kexp, A.vexp, A.seqlens, (Tout *)A.y, A.lse, A.Hq, p.chunk, p.nsplit, per_split, htiles, A.pg, parts, hdr, zs,
-        err);
+        ctl);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (p.nsplit == 1 && A.wacc == nullptr)) return e;
     const long combine = p.nsplit > 1 ? BH : 0;
@@ -640,10 +763,10 @@ cudaError_t launch_t(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, in
 }
 
 template <int D, bool Q8, typename Tout>
-cudaError_t launch_d(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, int *err, cudaStream_t s) {
-    if (A.rho == nullptr) return launch_t<D, Q8, false, 1, Tout>(A, p, ws, err, s);
-    if (A.pg.group <= 4) return launch_t<D, Q8, true, 1, Tout>(A, p, ws, err, s);
-    return launch_t<D, Q8, true, 2, Tout>(A, p, ws, err, s);
+cudaError_t launch_d(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, const DeviceCtl &ctl, cudaStream_t s) {
+    if (A.rho == nullptr) return launch_t<D, Q8, false, 1, Tout>(A, p, ws, ctl, s);
+    if (A.pg.group <= 4) return launch_t<D, Q8, true, 1, Tout>(A, p, ws, ctl, s);
+    return launch_t<D, Q8, true, 2, Tout>(A, p, ws, ctl, s);
 }
 
 }  // namespace
@@ -667,12 +790,12 @@ cudaError_t launch_decode_cache(const DecodeCacheArgs &A, const DecodePlan &p, v
     const bool f32 = A.out_dtype == PARALLAX_F32;
     if (A.d == 64) {
         if (A.kexp)
-            return f32 ? launch_d<64, true, float>(A, p, ws, ctl.err, s) : launch_d<64, true, __nv_bfloat16>(A, p, ws, ctl.err, s);
-        return f32 ? launch_d<64, false, float>(A, p, ws, ctl.err, s) : launch_d<64, false, __nv_bfloat16>(A, p, ws, ctl.err, s);
+            return f32 ? launch_d<64, true, float>(A, p, ws, ctl, s) : launch_d<64, true, __nv_bfloat16>(A, p, ws, ctl, s);
+        return f32 ? launch_d<64, false, float>(A, p, ws, ctl, s) : launch_d<64, false, __nv_bfloat16>(A, p, ws, ctl, s);
     }
     if (A.kexp)
-        return f32 ? launch_d<128, true, float>(A, p, ws, ctl.err, s) : launch_d<128, true, __nv_bfloat16>(A, p, ws, ctl.err, s);
-    return f32 ? launch_d<128, false, float>(A, p, ws, ctl.err, s) : launch_d<128, false, __nv_bfloat16>(A, p, ws, ctl.err, s);
+        return f32 ? launch_d<128, true, float>(A, p, ws, ctl, s) : launch_d<128, true, __nv_bfloat16>(A, p, ws, ctl, s);
+    return f32 ? launch_d<128, false, float>(A, p, ws, ctl, s) : launch_d<128, false, __nv_bfloat16>(A, p, ws, ctl, s);
 }
 
 }  // namespace plx

@@ -55,7 +55,10 @@ inline DecodePlan plan_decode_paged(int B, int Hq, int Hkv, int Tcap, int d, int
 // KV head and are sized like the paged decode's.
 inline DecodePlan plan_decode_cache(int B, int Hq, int Hkv, int heads, int Tcap, int d, int sm_count) {
     const int group = Hq / Hkv;
-    return plan_decode(B, Hkv * ((group + heads - 1) / heads) * 4, Tcap, d, sm_count);
+#ifndef UPS
+#define UPS 16
+#endif
+    return plan_decode(B, Hkv * ((group + heads - 1) / heads) * (64 / UPS), Tcap, d, sm_count);
 }
 
 }  // namespace plx

@@ -33,6 +33,7 @@ struct DeviceCtl {
     unsigned int debug_flags;       // test hooks (see DEBUG_*), 0 in normal use
 };
 constexpr unsigned DEBUG_FWD_SKIP_FIRST_K_LOAD = 1u;   // fwd: never load the first K tile
+constexpr unsigned DEBUG_DECODE_SKIP_FIRST_TILE = 2u;  // cache decode: never copy a warp's first tile
 
 // fp32 / bf16 CUDA-core forward (one warp per query row)
 cudaError_t launch_fwd_simt(const void *q, const void *k, const void *v, const void *rho, void *y, float *lse,

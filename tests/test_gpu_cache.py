@@ -642,3 +642,22 @@ def test_offsets_past_32_bits():
     for a, b in zip(*got):
         assert torch.equal(a, b)
     no_error()
+
+
+def test_forced_wait_timeout_is_reported_and_recoverable(monkeypatch):
+    """Test hook: no warp copies its first tile, so its bounded wait expires; the next call is right again."""
+    rng = np.random.default_rng(34)
+    c = Cache(rng, 2, 2, 16, 30, 128)
+    q = bf16(rng.standard_normal((2, 4, 128))).to(DEV)
+    sl = torch.tensor([480, 100], dtype=torch.int32, device=DEV)
+    ok, _ = plx.parallax_decode_paged_q8(q, q, c.kp, c.vp, c.ke, c.ve, c.tab, sl)
+    no_error()
+    monkeypatch.setenv("PARALLAX_DEBUG_FLAGS", "2")
+    monkeypatch.setenv("PARALLAX_WAIT_TIMEOUT_MS", "50")
+    plx.parallax_decode_paged_q8(q, q, c.kp, c.vp, c.ke, c.ve, c.tab, sl)
+    assert plx.parallax_last_device_error() == 7
+    monkeypatch.delenv("PARALLAX_DEBUG_FLAGS")
+    monkeypatch.delenv("PARALLAX_WAIT_TIMEOUT_MS")
+    y, _ = plx.parallax_decode_paged_q8(q, q, c.kp, c.vp, c.ke, c.ve, c.tab, sl)
+    no_error()
+    assert torch.equal(y, ok)
