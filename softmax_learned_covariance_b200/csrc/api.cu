@@ -132,9 +132,9 @@ int ensure_encoder() {
     return PARALLAX_OK;
 }
 
-// Row-major tensor seen as up to 3 dims (inner first), 128-byte swizzled boxes.
+// Row-major tensor seen as up to 3 dims (inner first), swizzled boxes (128-byte rows by default).
 int encode(CUtensorMap *m, CUtensorMapDataType dt, const void *base, int rank, const uint64_t *dims,
-           const uint32_t *box, uint32_t elem_bytes) {
+           const uint32_t *box, uint32_t elem_bytes, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     cuuint64_t gdim[3], gstride[2];
     cuuint32_t gbox[3], estr[3] = {1, 1, 1};
     uint64_t stride = elem_bytes;
@@ -145,7 +145,7 @@ int encode(CUtensorMap *m, CUtensorMapDataType dt, const void *base, int rank, c
         stride *= dims[i];
     }
     CUresult r = g_encode(m, dt, (cuuint32_t)rank, const_cast<void *>(base), gdim, gstride, gbox, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PARALLAX_OK : PARALLAX_ERR_CUDA;
 }
@@ -483,7 +483,7 @@ int decode_cache_impl(const void *q, const void *rho, const void *kpages, const 
                       const signed char *vexp, const int *block_table, const int *seqlens, void *y, float *lse,
                       float *wacc, int B, int Hq, int Hkv, int page_size, int max_pages, int num_pages, int d,
                       int in_dtype, int out_dtype, parallax_stream_t stream) {
-    DecodeCacheArgs A{q, rho, kpages, vpages, kexp, vexp, {}, seqlens, y, lse, wacc, B, Hq, d, out_dtype};
+    DecodeCacheArgs A{{}, {}, q, rho, kexp, vexp, {}, seqlens, y, lse, wacc, B, Hq, d, out_dtype};
     int st = paged_layout(block_table, B, Hkv, page_size, max_pages, num_pages, d, &A.pg);
     if (st) return st;
     if (Hq < Hkv || Hq % Hkv != 0 || (long long)B * Hq > (1ll << 28)) return PARALLAX_ERR_SHAPE;
@@ -496,13 +496,19 @@ int decode_cache_impl(const void *q, const void *rho, const void *kpages, const 
         return PARALLAX_ERR_DTYPE;
     DevState *s = nullptr;
     if ((st = get_state(&s))) return st;
-    const DecodePlan plan = plan_decode_cache(B, Hq, Hkv, decode_cache_heads(rho != nullptr, A.pg.group),
-                                              max_pages * page_size, d, s->sms);
-    const DecodeCacheScratch need = decode_cache_scratch(A, plan);
-    void *ws = nullptr;
+    if ((st = ensure_encoder())) return st;
+    const bool bf16 = kexp == nullptr;
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)page_size, (uint64_t)num_pages * Hkv};
+    const uint32_t box[3] = {(uint32_t)decode_cache_box(d, bf16), 16, 1};
+    const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapSwizzle sw = !bf16 && d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if ((st = encode(&A.tmk, dt, kpages, 3, dims, box, bf16 ? 2 : 1, sw))) return st;
+    if ((st = encode(&A.tmv, dt, vpages, 3, dims, box, bf16 ? 2 : 1, sw))) return st;
+    const DecodeCacheScratch need = decode_cache_scratch(A, s->sms);
+    void *mem = nullptr;
     CallScratch scratch(s, static_cast<cudaStream_t>(stream));
-    if ((st = scratch.get(need.parts + need.hdr + need.zs, &ws))) return st;
-    return status_of(launch_decode_cache(A, plan, ws, make_ctl(s), static_cast<cudaStream_t>(stream)));
+    if ((st = scratch.get(need.bytes(), &mem))) return st;
+    return status_of(launch_decode_cache(A, need, mem, make_ctl(s), static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

@@ -17,15 +17,18 @@
 // weights into the second product's operand.
 //
 // Each warp streams its own 16-token tiles through a ring in shared memory that
-// bulk copies (TMA) fill: K and V in four pieces of four tokens each, 32 bytes
-// apart from multiples of 128, which makes the threads' 16-byte reads free of
-// bank conflicts.  The order of the contracted index is free as long as both
-// operands agree, so a thread reads whole 16-byte chunks and uses them as its
-// part of the fragments (K: chunks of its own two tokens; V: the same chunk of
-// its four tokens): no ldmatrix and no barrier beyond the warp's own mbarriers.
+// TMA fills, one box of 16 rows each for K and V (two for 256-byte rows).  The
+// order of the contracted index is free as long as both operands agree, so a
+// thread reads whole 16-byte chunks and uses them as its part of the fragments
+// (K: chunks of its own two tokens; V: the same chunk of its four tokens): no
+// ldmatrix, and no barrier beyond the warp's own mbarriers.  The order of the
+// tokens is free too; with the hardware's swizzle it is chosen so that no read
+// has a bank conflict (row_of).
 // The loads bound the kernel and how they are issued decides their rate (B=64,
 // 16 heads of their own, 4096 tokens, d = 128, 1.07 GB; loads alone): 16-byte
-// cp.async in fragment order 205 us, in row order 196 us, bulk copies 168 us.
+// cp.async in fragment order 205 us, in row order 196 us, bulk copies 168 us;
+// bulk copies of padded four-row pieces cost the warps 10 us more to issue than
+// whole tiles.
 //
 // Numerics.  e4m3 codes are exact in fp16; q and rho are brought to fp16 by a
 // power of two per vector (exact down to 2^-22 of the vector's largest
@@ -39,6 +42,7 @@
 #include <type_traits>
 
 #include "cache_common.cuh"
+#include "decode_sched.h"
 #include "sm100.cuh"
 
 namespace plx {
@@ -54,9 +58,8 @@ constexpr int WARPS = 4;
 #ifndef MINB
 #define MINB 4
 #endif
-#ifndef UPS
-#define UPS 16
-#endif
+// Tables of at most this many tokens: one CTA per item, no merge.
+constexpr int WHOLE_TOKENS = 256;
 constexpr float MNONE = -1e30f;     // reference of a row that has seen no score
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -71,12 +74,6 @@ __device__ __forceinline__ float fex2(float x) {
     return r;
 }
 
-// `bytes` (a multiple of 16) from global to shared memory; completion is counted on `bar`
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <bool Q8>
@@ -126,8 +123,19 @@ template <> __device__ __forceinline__ void store_y<__nv_bfloat16>(__nv_bfloat16
 
 constexpr int BAD = 1 << 16;     // a tile's page id is out of range
 
-// row in its piece of the x-th of a thread's four value tokens: columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9
-__device__ __forceinline__ constexpr int x_row(int x) { return (x & 1) + 2 * (x >> 1); }
+// Token of row i < 8 of the products' 16-row operand (row i + 8: the token + 8).
+// A shared-memory phase is 8 threads of 16 bytes, rows 2 m and 2 m + 1 by four chunks
+// of K, or chunks 2 m and 2 m + 1 by the rows 0, 2, 4, 6 or 1, 3, 5, 7 of V; each has
+// to hit all 8 chunk columns once.  128-byte rows are swizzled by row & 7, 64-byte
+// rows (two to a line; a V phase is 16 threads of 8 bytes) by (row >> 1) & 3.
+template <int RB> __device__ __forceinline__ constexpr int row_of(int i) {
+    if (RB == 64) return (i & 4) | ((i & 1) ? 3 - ((i >> 1) & 1) : (i >> 1) & 1);      // 0 3 1 2 4 7 5 6
+    return (i & 1) ? i ^ 4 : i;                                                         // 0 5 2 7 4 1 6 3
+}
+// byte of 16-byte chunk c of row `row` of a swizzled box
+template <int RB> __device__ __forceinline__ constexpr int chunk_at(int row, int c) {
+    return row * RB + ((c ^ (RB == 64 ? (row >> 1) & 3 : row & 7)) << 4);
+}
 
 // Shapes of one instantiation.  NT n-tiles of 8 vectors: 4 NT heads with a
 // probe, 8 NT without.
@@ -143,62 +151,132 @@ template <int D, bool Q8, bool RHO, int NT> struct Shape {
     // state of a warp in the merge: per head m, l, abar, then O[D] (and M[D])
     static constexpr int MSTRIDE = (RHO ? 2 : 1) * D + 4;
     static constexpr int MERGE_BYTES = WARPS * HEADS * MSTRIDE * 4;
-    // K or V of 16 tokens: four pieces of four rows, 32 bytes off a multiple of 128
-    static constexpr int PIECE = 4 * ROW + 32;
-    static constexpr int TILE_BYTES = 2 * 4 * PIECE;
-    // Token of a thread's score rows r = 2 m + o and r + 8: row o (and o + 2) of piece m,
-    // or, for the odd rows of 128-byte and wider rows, of the piece 64 bytes further in
-    // the banks; so the 8 threads of a shared-memory phase read 8 different chunks.
-    static constexpr int ODD_PIECE = ROW == 64 ? 0 : 2;
+    static constexpr int RB = ROW < 128 ? ROW : 128;     // bytes of a box row (and of its swizzle)
+    static constexpr int BOXES = ROW / RB;               // boxes of a K or V tile
+    static constexpr int HALF = 16 * ROW;                // bytes of a K or V tile
+    static constexpr int TILE_BYTES = 2 * HALF;
     static constexpr int STAGES = Q8 ? Q8_STAGES : BF_STAGES;            // tiles in flight per warp: STAGES - 1
     static constexpr int RING_BYTES = WARPS * STAGES * TILE_BYTES;
-    static constexpr int SMEM = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
+    static constexpr int BAR_OFF = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
+    static constexpr int SMEM = BAR_OFF + 8 * WARPS * STAGES + 1024;     // and what aligning the base to 1024 takes
 };
 
-// Partials of a split unit: O[D] (and M[D]) per (b, h, split); its m, l, abar in `hdr`.
+// Floats of a cut item's part per head: O[D] (and M[D]).
 template <int D, bool RHO> constexpr int part_stride() { return (RHO ? 2 : 1) * D; }
+
+// Scratch of a call, in the order of DecodeCacheScratch.
+struct Scratch {
+    float *parts;       // [slot][HEADS][O, M]
+    float4 *hdr;        // [slot][HEADS] (m, l, abar) of the cut items' parts
+    int2 *cut;          // [CTA] (item, parts) of the item it starts but does not finish, or (-1, 0)
+    int2 *item;         // [item] (first CTA, parts), with weights
+    float *lse2;        // [B, Hq] log2 of an uncut item's sum, with weights
+    float *zs;          // [item][Tcap][HEADS] scores (log2), with weights
+};
 
 template <int D, bool Q8, bool RHO, int NT, typename Tout>
 __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cache(
-    const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ rho, const uint8_t *__restrict__ kp,
-    const uint8_t *__restrict__ vp, const signed char *__restrict__ kexp, const signed char *__restrict__ vexp,
-    const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse, int Hq, int chunk, int nsplit,
-    long units_per_split, int htiles, PagedKV pg, float *__restrict__ parts, float4 *__restrict__ hdr,
-    float *__restrict__ zs, DeviceCtl ctl) {
+    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+    const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ rho, const signed char *__restrict__ kexp,
+    const signed char *__restrict__ vexp, const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse,
+    int B, int Hq, int htiles, bool whole, PagedKV pg, Scratch ws, DeviceCtl ctl) {
     using S = Shape<D, Q8, RHO, NT>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023) & 1023);
     float *merge = reinterpret_cast<float *>(smem);
+    __shared__ int abort_flag;
+    __shared__ long long wsum[WARPS], sh_before;
+    __shared__ int sh_b;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t full = smem_u32(smem + S::BAR_OFF) + 8 * S::STAGES * warp;     // this warp's barriers, one per stage
     const int r = lane / 4, t4 = lane % 4;
     const float scale_log2 = LOG2E / sqrtf((float)D);
     const int ps = 1 << pg.pshift, pmask = ps - 1;
-    const long units = units_per_split * nsplit;
-    __shared__ uint64_t full[WARPS][S::STAGES];
-    __shared__ int abort_flag;
+    const int Tcap = pg.max_pages << pg.pshift;
+    const int per_seq = pg.Hkv * htiles;     // items of a sequence
+    auto len_of = [&](int i) { return min(max(seqlens[i], 0), Tcap); };
+
+    // ---- this CTA's range of quads: from quad `q0` of item `it` of sequence `b`, `left` quads ----
+    int b, it, q0 = 0, cta = 0, nctas = 1;
+    long long left, pos = 0, total = 1;
+    if (whole) {                             // one item per CTA
+        b = blockIdx.x / per_seq;
+        it = blockIdx.x % per_seq;
+        left = quads_of(len_of(b));
+    } else {
+        // prefix sums of the sequences' quads: a run of sequences per thread, then over the threads
+        const int run = (B + WARPS * 32 - 1) / (WARPS * 32);
+        const int b0 = min((int)threadIdx.x * run, B), b1 = min(b0 + run, B);
+        long long own = 0;
+        for (int i = b0; i < b1; ++i) own += quads_of(len_of(i));
+        long long incl = own;
+#pragma unroll
+        for (int off = 1; off < 32; off *= 2) {
+            const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        long long all = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (w == warp) incl += all;
+            all += wsum[w];
+        }
+        total = all * per_seq;
+        cta = blockIdx.x;
+        nctas = sched_ctas(total, gridDim.x);
+        if (threadIdx.x == 0) ws.cut[cta] = make_int2(-1, 0);
+        if (cta >= nctas) {
+            left = 0;
+        } else {
+            pos = sched_start(cta, total, nctas);
+            left = sched_start(cta + 1, total, nctas) - pos;
+            long long before = incl - own;
+            if (before * per_seq <= pos && pos < incl * per_seq) {
+                int i = b0;
+                for (int n; (before + (n = quads_of(len_of(i)))) * per_seq <= pos; ++i) before += n;
+                sh_b = i;
+                sh_before = before;
+            }
+            __syncthreads();
+            b = sh_b;
+            const long long rem = pos - sh_before * per_seq;
+            const int n = quads_of(len_of(b));
+            it = (int)(rem / n);
+            q0 = (int)(rem % n);
+        }
+    }
+    // sequences without a token: nothing else writes their rows
+    for (int e = whole ? b : (int)blockIdx.x; e < B; e += whole ? B : (int)gridDim.x) {
+        if (len_of(e) > 0 || (whole && it != 0)) continue;
+        for (int i = threadIdx.x; i < Hq * D; i += WARPS * 32) store_y<Tout>(y + (size_t)e * Hq * D + i, 0.f);
+        if (lse != nullptr)
+            for (int i = threadIdx.x; i < Hq; i += WARPS * 32) lse[(size_t)e * Hq + i] = -INFINITY;
+    }
+    if (left == 0) return;
+
     if (threadIdx.x == 0) abort_flag = 0;
     if (lane == 0)
-        for (int i = 0; i < S::STAGES; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(full + 8 * i, 1);
     fence_mbar_init();
     __syncthreads();
     const WaitCtl wait{ctl.err, &abort_flag, ctl.wait_ns};
     int stage = 0;               // stage of this warp's next tile
     uint32_t phases = 0;         // parity each stage's barrier completes next
 
-    for (long u = blockIdx.x; u < units; u += gridDim.x) {
-        const long ut = u % units_per_split;    // chunk-major
-        const int split = (int)(u / units_per_split);
-        const int b = (int)(ut / ((long)pg.Hkv * htiles));
-        const int rem = (int)(ut % ((long)pg.Hkv * htiles));
-        const int kvh = rem / htiles, ht = rem % htiles;
+    while (true) {
+        const int L = len_of(b), nq = quads_of(L);
+        const int q1 = (int)min((long long)nq, q0 + left);
+        const int kvh = it / htiles, ht = it % htiles;
         const int g0 = ht * S::HEADS;
         const int nh = min(S::HEADS, pg.group - g0);
         const long h0 = (long)b * Hq + (long)kvh * pg.group + g0;
-        const int Tcap = pg.max_pages << pg.pshift;
-        const int L = min(max(seqlens[b], 0), Tcap);
-        const int t0 = split * chunk;
-        if (t0 >= L && nsplit > 1) continue;
-        const int t1 = min(L, t0 + chunk);
+        const long item = (long)b * per_seq + it;
+        const int t0 = q0 * QUAD;
+        const int t1 = min(L, q1 * QUAD);
         const int ntiles = (t1 - t0 + 15) / 16;
+        const bool uncut = q0 == 0 && q1 == nq;
 
         // ---- the vectors: column n = r of n-tile nt; 4 elements per MMA step ----
         uint32_t qf[NT][S::KSTEPS][2];
@@ -286,21 +364,22 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
         int ids = page_of(lane), ids_next = 0, info = info_of(lane, ids), info_next = 0;
 
         uint8_t *ring = smem + warp * S::STAGES * S::TILE_BYTES;
-        // copies tile j from page `id` into stage st, lane l < 8 one piece of K (l < 4) or V;
-        // rows past t1, and all rows of a bad page, are left out
+        // loads tile j from page `id` into stage st; the rows of a bad page are not loaded
         auto issue = [&](int j, int st, int id) {
             const int t = t0 + (warp + WARPS * j) * 16;
             const bool ok = (unsigned)id < (unsigned)pg.num_pages;
-            const int rows = ok ? min(16, t1 - t) : 0;
-            const uint32_t bar = smem_u32(&full[warp][st]);
-            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * rows * S::ROW);
-            __syncwarp();
-            const int piece = lane & 3, n = min(rows - 4 * piece, 4);
-            const bool skip = (ctl.debug_flags & DEBUG_DECODE_SKIP_FIRST_TILE) != 0 && j == 0;
-            if (lane < 8 && n > 0 && !skip) {
-                const size_t row = (((size_t)id * pg.Hkv + kvh) << pg.pshift) + (t & pmask) + 4 * piece;
-                bulk_load(smem_u32(ring + st * S::TILE_BYTES + lane * S::PIECE), (lane < 4 ? kp : vp) + row * S::ROW,
-                          n * S::ROW, bar);
+            __syncwarp();                        // every lane has read what the stage held
+            if (lane == 0) {
+                mbar_arrive_expect_tx(full + 8 * st, ok ? S::TILE_BYTES : 0);
+                if (ok && !((ctl.debug_flags & DEBUG_DECODE_SKIP_FIRST_TILE) && j == 0)) {
+                    const uint32_t dst = smem_u32(ring + st * S::TILE_BYTES);
+                    const int row = t & pmask, slab = id * pg.Hkv + kvh;
+#pragma unroll
+                    for (int x = 0; x < S::BOXES; ++x) {
+                        tma_load_3d(dst + x * 16 * S::RB, &tmk, full + 8 * st, x * (S::RB / S::EL), row, slab);
+                        tma_load_3d(dst + S::HALF + x * 16 * S::RB, &tmv, full + 8 * st, x * (S::RB / S::EL), row, slab);
+                    }
+                }
             }
         };
 #pragma unroll
@@ -309,10 +388,11 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
             if (j < mine) issue(j, (stage + j) % S::STAGES, id);
         }
         // where this thread's tokens and chunks lie in a tile
-        const int tok0 = 4 * ((r / 2 + (r & 1) * S::ODD_PIECE) & 3) + (r & 1), tok1 = tok0 + 2;
-        const uint32_t koff = (tok0 / 4) * S::PIECE + (tok0 & 3) * S::ROW + 16 * t4;
-        const int vpiece[2] = {t4, (t4 + S::ODD_PIECE) & 3};
-        const uint32_t voff = (S::VB < 16 ? S::VB : 16) * r;
+        const int tok0 = row_of<S::RB>(r), tok1 = tok0 + 8;
+        const int koff = chunk_at<S::RB>(tok0, t4);
+        const int va = row_of<S::RB>(2 * t4), vb = row_of<S::RB>(2 * t4 + 1);
+        const int vc = S::VB < 16 ? r / 2 : r, vsub = S::VB < 16 ? 8 * (r & 1) : 0;
+        const int voff[2] = {S::HALF + chunk_at<S::RB>(va, vc) + vsub, S::HALF + chunk_at<S::RB>(vb, vc) + vsub};
         for (int j = 0; j < mine; ++j) {
             // ---- pages and exponents of the 32 tiles after these, in good time ----
             if ((j & 31) == 0)
@@ -329,21 +409,28 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
                 ids = ids_next;
                 info = info_next;
             }
-            const bool landed = mbar_wait(smem_u32(&full[warp][stage]), (phases >> stage) & 1u, wait);
+            const bool landed = mbar_wait(full + 8 * stage, (phases >> stage) & 1u, wait);
             if (!__all_sync(0xffffffffu, landed)) {
                 // give up: let this warp's copies land (bounded) before the CTA's memory goes
                 for (int i = j; i < min(jn + 1, mine); ++i) {
                     const int st = (stage + i - j) % S::STAGES;
-                    mbar_wait_drain(smem_u32(&full[warp][st]), (phases >> st) & 1u, 2000000ull);
+                    mbar_wait_drain(full + 8 * st, (phases >> st) & 1u, 2000000ull);
                 }
                 break;
             }
             phases ^= 1u << stage;
-            const uint8_t *dk = ring + stage * S::TILE_BYTES, *dv = dk + 4 * S::PIECE;
+            uint8_t *dk = ring + stage * S::TILE_BYTES;
             stage = stage + 1 == S::STAGES ? 0 : stage + 1;
             const int tile = t0 + (warp + WARPS * j) * 16;
             const int nvalid = t1 - tile;                   // tokens of the tile
-            const int nread = now & BAD ? 0 : nvalid;       // rows of it that were copied
+            if (nvalid < 16 || (now & BAD)) {
+                // rows past the sequence hold whatever the page does, those of a bad page what the
+                // stage held: zeros, as a weight of 0 times NaN is no 0
+                for (int i = lane; i < S::TILE_BYTES / 16; i += 32)
+                    if (i * 16 / S::RB % 16 >= nvalid || (now & BAD)) reinterpret_cast<uint4 *>(dk)[i] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async();               // before a later load into this stage
+                __syncwarp();
+            }
 
             // ---- scores ----
             float sc[NT][4], sc2[NT][4];          // two chains of products
@@ -353,12 +440,9 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
                 for (int e = 0; e < 4; ++e) sc[nt][e] = sc2[nt][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < S::KC; ++c) {
-                uint4 k0 = *reinterpret_cast<const uint4 *>(dk + koff + 64 * c);
-                uint4 k1 = *reinterpret_cast<const uint4 *>(dk + koff + 2 * S::ROW + 64 * c);
-                if (nread < 16) {                           // what was not copied is not looked at
-                    if (tok0 >= nread) k0 = make_uint4(0u, 0u, 0u, 0u);
-                    if (tok1 >= nread) k1 = make_uint4(0u, 0u, 0u, 0u);
-                }
+                const uint8_t *src = dk + (c / 2) * 16 * S::RB + (koff ^ ((c & 1) << 6));
+                const uint4 k0 = *reinterpret_cast<const uint4 *>(src);
+                const uint4 k1 = *reinterpret_cast<const uint4 *>(src + 8 * S::RB);
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                 for (int i = 0; i < (Q8 ? 4 : 2); ++i) {
@@ -399,8 +483,8 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
                 }
                 up |= fmaxf(dz[h][0], dz[h][1]) > HEADROOM;
             }
-            if (zs != nullptr) {
-                float *dst = zs + ((((size_t)b * pg.Hkv + kvh) * htiles + ht) * (size_t)Tcap + tile) * S::HEADS;
+            if (ws.zs != nullptr) {
+                float *dst = ws.zs + ((size_t)item * Tcap + tile) * S::HEADS;
 #pragma unroll
                 for (int h = 0; h < S::HPT; ++h) {
                     const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
@@ -478,7 +562,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
                 uint32_t v[4][4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {       // tokens of the weights' columns 2 t4, 2 t4 + 1, + 8, + 9
-                    const uint8_t *src = dv + vpiece[x & 1] * S::PIECE + x_row(x) * S::ROW + voff + 128 * c;
+                    const uint8_t *src = dk + c * 16 * S::RB + voff[x & 1] + 8 * (x >> 1) * S::RB;
                     if constexpr (S::VB < 16) {
                         const uint2 w = *reinterpret_cast<const uint2 *>(src);
                         v[x][0] = w.x;
@@ -490,7 +574,6 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
                         v[x][2] = w.z;
                         v[x][3] = w.w;
                     }
-                    if (nread < 16 && 4 * vpiece[x & 1] + x_row(x) >= nread) v[x][0] = v[x][1] = v[x][2] = v[x][3] = 0u;
                 }
                 constexpr int PER = S::JS / ((S::VB + 15) / 16);      // MMAs of a chunk
 #pragma unroll
@@ -577,59 +660,75 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
                 }
             }
             const long bh = h0 + hh;
-            if (nsplit == 1) {
-                float out = 0.f;
-                if (ntiles > 0) {
-                    const float inv = 1.0f / l;
-                    out = o * inv;
-                    if constexpr (RHO) out -= m * inv - out * (ab * inv);
-                }
+            if (uncut) {
+                const float inv = 1.0f / l;
+                float out = o * inv;
+                if constexpr (RHO) out -= m * inv - out * (ab * inv);
                 store_y<Tout>(y + bh * D + e, out);
-                if (e == 0 && lse != nullptr) lse[bh] = ntiles > 0 ? (mu + log2f(l)) * LN2 : -INFINITY;
+                if (e == 0) {
+                    const float l2 = mu + log2f(l);
+                    if (lse != nullptr) lse[bh] = l2 * LN2;
+                    if (ws.lse2 != nullptr) ws.lse2[bh] = l2;
+                }
             } else {
-                float *P = parts + ((size_t)bh * nsplit + split) * part_stride<D, RHO>();
+                const int slot = sched_slot(cta, q0 == 0) * S::HEADS + hh;
+                float *P = ws.parts + (size_t)slot * part_stride<D, RHO>();
                 P[e] = o;
                 if constexpr (RHO) P[D + e] = m;
+                if (e == 0) ws.hdr[slot] = make_float4(mu, l, ab, 0.f);
             }
-            if (e == 0 && hdr != nullptr) hdr[bh * nsplit + split] = make_float4(mu, l, ab, 0.f);
         }
-        fence_proxy_async();   // the next unit's copies write where these stores and loads went
+        if (q0 == 0 && threadIdx.x == 0) {
+            const int parts = uncut ? 1 : sched_owner(pos + nq - 1, total, nctas) - cta + 1;
+            if (!uncut) ws.cut[cta] = make_int2((int)item, parts);
+            if (ws.item != nullptr) ws.item[item] = make_int2(cta, parts);
+        }
+        left -= q1 - q0;
+        if (left == 0) break;
+        pos += q1 - q0;
+        q0 = 0;
+        if (++it == per_seq) {
+            it = 0;
+            do ++b;
+            while (len_of(b) == 0);
+        }
+        fence_proxy_async();   // the next item's copies write where these stores and loads went
         __syncthreads();
     }
 }
 
-// One launch after the split kernel: blocks [0, combine_blocks) merge the splits
-// of one (b, h) each and write y and lse; the others add the weights
-// s = 2^(z - lse2) of ACC_TOKENS tokens of one (b, kvh) to the accumulator, summed
-// over the KV head's query heads in head order (each token by one thread:
-// the result does not depend on the schedule).
+// One launch after the decode: the first blocks, HEADS per CTA of the decode, merge
+// the parts of the item that CTA starts but does not finish (one head each) and
+// write y and lse; the others add the weights s = 2^(z - lse2) of ACC_TOKENS
+// tokens of one (b, kvh) to the accumulator, summed over the KV head's query
+// heads in head order (each token by one thread: the result does not depend on
+// the schedule).
 constexpr int FIN_THREADS = 256;
 constexpr int ACC_TOKENS = 1024;
 
 template <int D, bool RHO, int HEADS, typename Tout>
 __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
-    const float *__restrict__ parts, const float4 *__restrict__ hdr, const float *__restrict__ zs,
-    const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse, float *__restrict__ wacc, int Hq,
-    int Hkv, int htiles, int chunk, int nsplit, int Tcap, long combine_blocks, int acc_chunks) {
-    constexpr int COLS = (RHO ? 2 : 1) * D / 4;               // float4 columns of a partial
-    constexpr int GROUPS = FIN_THREADS / COLS;                // splits in flight
+    Scratch ws, const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse, float *__restrict__ wacc,
+    int Hq, int Hkv, int htiles, int Tcap, int ctas, int combine_blocks, int acc_chunks) {
+    constexpr int COLS = (RHO ? 2 : 1) * D / 4;               // float4 columns of a part
+    constexpr int GROUPS = FIN_THREADS / COLS;                // parts in flight
     __shared__ float4 red[GROUPS][COLS];
     __shared__ float2 redl[GROUPS];
     __shared__ float wred[FIN_THREADS / 32];
     __shared__ float slse[HEADS];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    if ((long)blockIdx.x < combine_blocks) {
-        const long bh = blockIdx.x;
-        const int L = min(max(seqlens[bh / Hq], 0), Tcap);
-        const int nv = (L + chunk - 1) / chunk;
-        if (nv == 0) {
-            for (int e = tid; e < D; e += FIN_THREADS) store_y<Tout>(y + bh * D + e, 0.f);
-            if (lse != nullptr && tid == 0) lse[bh] = -INFINITY;
-            return;
-        }
-        const float4 *H = hdr + bh * nsplit;
+    const int group = Hq / Hkv;
+    if ((int)blockIdx.x < combine_blocks) {
+        const int c0 = blockIdx.x / HEADS, hh = blockIdx.x % HEADS;
+        const int2 cut = ws.cut[c0];
+        if (cut.x < 0) return;
+        const int per_seq = Hkv * htiles, b = cut.x / per_seq, it = cut.x % per_seq;
+        const int g = (it % htiles) * HEADS + hh;
+        if (g >= group) return;
+        const long bh = (long)b * Hq + (long)(it / htiles) * group + g;
+        const int nv = cut.y;
         float mu = -INFINITY;
-        for (int s = tid; s < nv; s += FIN_THREADS) mu = fmaxf(mu, H[s].x);
+        for (int s = tid; s < nv; s += FIN_THREADS) mu = fmaxf(mu, ws.hdr[sched_part(c0, s) * HEADS + hh].x);
 #pragma unroll
         for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
         if (lane == 0) wred[warp] = mu;
@@ -639,11 +738,12 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
         const int col = tid % COLS, grp = tid / COLS;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         float l = 0.f, ab = 0.f;
-        const float4 *P = reinterpret_cast<const float4 *>(parts) + (size_t)bh * nsplit * COLS + col;
+        const float4 *P = reinterpret_cast<const float4 *>(ws.parts) + col;
 #pragma unroll 4
         for (int s = grp; s < nv; s += GROUPS) {
-            const float4 h = H[s];
-            const float4 p = P[(size_t)s * COLS];
+            const int slot = sched_part(c0, s) * HEADS + hh;
+            const float4 h = ws.hdr[slot];
+            const float4 p = P[(size_t)slot * COLS];
             const float w = fex2(h.x - mu);
             l = fmaf(w, h.y, l);
             ab = fmaf(w, h.z, ab);
@@ -657,18 +757,18 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
         __syncthreads();
         l = ab = 0.f;
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            l += redl[g].x;
-            ab += redl[g].y;
+        for (int i = 0; i < GROUPS; ++i) {
+            l += redl[i].x;
+            ab += redl[i].y;
         }
         const float inv = 1.f / l;
         const float *R = reinterpret_cast<const float *>(red);
         for (int e = tid; e < D; e += FIN_THREADS) {
             float o = 0.f, m = 0.f;
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                o += R[g * COLS * 4 + e];
-                if constexpr (RHO) m += R[g * COLS * 4 + D + e];
+            for (int i = 0; i < GROUPS; ++i) {
+                o += R[i * COLS * 4 + e];
+                if constexpr (RHO) m += R[i * COLS * 4 + D + e];
             }
             float out = o * inv;
             if constexpr (RHO) out -= m * inv - out * (ab * inv);
@@ -678,49 +778,63 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
         return;
     }
     // ---- accumulate ----
-    const long ab_ = (long)blockIdx.x - combine_blocks;
-    const int ck = (int)(ab_ % acc_chunks);
-    const long bk = ab_ / acc_chunks;                          // b * Hkv + kvh
-    const int b = (int)(bk / Hkv), kvh = (int)(bk % Hkv), group = Hq / Hkv;
+    const long rest = (long)blockIdx.x - combine_blocks;
+    const int ck = (int)(rest % acc_chunks);
+    const long bk = rest / acc_chunks;                         // b * Hkv + kvh
+    const int b = (int)(bk / Hkv), kvh = (int)(bk % Hkv);
     const int L = min(max(seqlens[b], 0), Tcap);
     const int t0 = ck * ACC_TOKENS;
     if (t0 >= L) return;
-    const int nv = (L + chunk - 1) / chunk;
     constexpr int PER = ACC_TOKENS / FIN_THREADS;
     float sum[PER];
 #pragma unroll
     for (int k = 0; k < PER; ++k) sum[k] = 0.f;
     for (int ht = 0; ht < htiles; ++ht) {
         const int nh = min(HEADS, group - ht * HEADS);
-        __syncthreads();
-        for (int h = warp; h < nh; h += FIN_THREADS / 32) {
-            const float4 *H = hdr + ((long)b * Hq + (long)kvh * group + ht * HEADS + h) * nsplit;
-            float mu = -INFINITY, l = 0.f;
-            for (int s = lane; s < nv; s += 32) mu = fmaxf(mu, H[s].x);
+        const long item = bk * htiles + ht;
+        // the scores do not wait for the sums
+        float4 z[PER][HEADS / 4];
 #pragma unroll
-            for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
-            for (int s = lane; s < nv; s += 32) l += fex2(H[s].x - mu) * H[s].y;
-#pragma unroll
-            for (int off = 16; off > 0; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
-            if (lane == 0) slse[h] = mu + log2f(l);
-        }
-        __syncthreads();
-        const float *Z = zs + (((size_t)bk * htiles + ht) * (size_t)Tcap) * HEADS;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int t = t0 + tid + k * FIN_THREADS;
-            if (t >= L) continue;
-            const float4 *zr = reinterpret_cast<const float4 *>(Z + (size_t)t * HEADS);
+        for (int k = 0; k < PER; ++k)
 #pragma unroll
             for (int c = 0; c < HEADS / 4; ++c) {
-                if (4 * c >= nh) break;
-                const float4 zv = zr[c];
-                sum[k] += fex2(zv.x - slse[4 * c]);
-                if (4 * c + 1 < nh) sum[k] += fex2(zv.y - slse[4 * c + 1]);
-                if (4 * c + 2 < nh) sum[k] += fex2(zv.z - slse[4 * c + 2]);
-                if (4 * c + 3 < nh) sum[k] += fex2(zv.w - slse[4 * c + 3]);
+                const int t = t0 + tid + k * FIN_THREADS;
+                z[k][c] = t < L ? reinterpret_cast<const float4 *>(ws.zs + ((size_t)item * Tcap + t) * HEADS)[c]
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
             }
+        int2 info = ws.item[item];
+        // a decode that gave up on a wait has not written it: whatever is read stays in bounds
+        if (info.y != 1 && (info.x < 0 || info.x >= ctas || info.y < 1 || info.y > ctas - info.x)) info = make_int2(0, 1);
+        __syncthreads();
+        for (int h = warp; h < nh; h += FIN_THREADS / 32) {
+            float l2;
+            if (info.y == 1) {
+                l2 = ws.lse2[(long)b * Hq + (long)kvh * group + ht * HEADS + h];
+            } else {
+                float mu = -INFINITY, l = 0.f;
+                for (int s = lane; s < info.y; s += 32) mu = fmaxf(mu, ws.hdr[sched_part(info.x, s) * HEADS + h].x);
+#pragma unroll
+                for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
+                for (int s = lane; s < info.y; s += 32) {
+                    const float4 p = ws.hdr[sched_part(info.x, s) * HEADS + h];
+                    l += fex2(p.x - mu) * p.y;
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
+                l2 = mu + log2f(l);
+            }
+            if (lane == 0) slse[h] = l2;
         }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int c = 0; c < HEADS / 4; ++c) {
+                const float zv[4] = {z[k][c].x, z[k][c].y, z[k][c].z, z[k][c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * c + i < nh) sum[k] += fex2(zv[i] - slse[4 * c + i]);
+            }
     }
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -733,69 +847,82 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
 template <bool RHO> int heads_for(int group) { return RHO ? (group <= 4 ? 4 : 8) : 8; }
 
 template <int D, bool Q8, bool RHO, int NT, typename Tout>
-cudaError_t launch_t(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, const DeviceCtl &ctl, cudaStream_t s) {
+cudaError_t launch_t(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, void *mem, const DeviceCtl &ctl,
+                     cudaStream_t s) {
     using S = Shape<D, Q8, RHO, NT>;
     const int htiles = (A.pg.group + S::HEADS - 1) / S::HEADS;
     const int Tcap = A.pg.max_pages << A.pg.pshift;
-    const long BH = (long)A.B * A.Hq;
-    const DecodeCacheScratch sc = decode_cache_scratch(A, p);
-    char *base = static_cast<char *>(ws);
-    float *parts = sc.parts ? reinterpret_cast<float *>(base) : nullptr;
-    float4 *hdr = sc.hdr ? reinterpret_cast<float4 *>(base + sc.parts) : nullptr;
-    float *zs = sc.zs ? reinterpret_cast<float *>(base + sc.parts + sc.hdr) : nullptr;
-    const long per_split = (long)A.B * A.pg.Hkv * htiles;
-    const long units = per_split * p.nsplit;
+    char *at = static_cast<char *>(mem);
+    auto take = [&](size_t n) {
+        char *p = n ? at : nullptr;
+        at += n;
+        return p;
+    };
+    Scratch ws;
+    ws.parts = reinterpret_cast<float *>(take(sc.parts));
+    ws.hdr = reinterpret_cast<float4 *>(take(sc.hdr));
+    ws.cut = reinterpret_cast<int2 *>(take(sc.cut));
+    ws.item = reinterpret_cast<int2 *>(take(sc.item));
+    ws.lse2 = reinterpret_cast<float *>(take(sc.lse2));
+    ws.zs = reinterpret_cast<float *>(take(sc.zs));
+    const bool whole = sc.ctas == 0;
+    const int grid = whole ? A.B * A.pg.Hkv * htiles : sc.ctas;
     static std::atomic<unsigned long long> limit_set{0};
     if (cudaError_t e = ensure_smem_limit(k_decode_cache<D, Q8, RHO, NT, Tout>, S::SMEM, limit_set)) return e;
-    k_decode_cache<D, Q8, RHO, NT, Tout><<<(unsigned)(units < 0x7fffffffL ? units : 0x7fffffffL), WARPS * 32, S::SMEM, s>>>(
-        (const __nv_bfloat16 *)A.q, (const __nv_bfloat16 *)A.rho, (const uint8_t *)A.kpages, (const uint8_t *)A.vpages,
-        A.kexp, A.vexp, A.seqlens, (Tout *)A.y, A.lse, A.Hq, p.chunk, p.nsplit, per_split, htiles, A.pg, parts, hdr, zs,
-        ctl);
+    k_decode_cache<D, Q8, RHO, NT, Tout><<<grid, WARPS * 32, S::SMEM, s>>>(
+        A.tmk, A.tmv, (const __nv_bfloat16 *)A.q, (const __nv_bfloat16 *)A.rho, A.kexp, A.vexp, A.seqlens, (Tout *)A.y, A.lse, A.B, A.Hq, htiles, whole, A.pg, ws, ctl);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || (p.nsplit == 1 && A.wacc == nullptr)) return e;
-    const long combine = p.nsplit > 1 ? BH : 0;
+    if (e != cudaSuccess || (whole && A.wacc == nullptr)) return e;
+    const int combine = whole ? 0 : grid * S::HEADS;
     const int acc_chunks = A.wacc ? (Tcap + ACC_TOKENS - 1) / ACC_TOKENS : 0;
     const long blocks = combine + (long)A.B * A.pg.Hkv * acc_chunks;
     k_decode_finish<D, RHO, S::HEADS, Tout><<<(unsigned)blocks, FIN_THREADS, 0, s>>>(
-        parts, hdr, zs, A.seqlens, (Tout *)A.y, A.lse, A.wacc, A.Hq, A.pg.Hkv, htiles, p.chunk, p.nsplit, Tcap, combine,
-        acc_chunks);
+        ws, A.seqlens, (Tout *)A.y, A.lse, A.wacc, A.Hq, A.pg.Hkv, htiles, Tcap, sc.ctas, combine, acc_chunks);
     return cudaGetLastError();
 }
 
 template <int D, bool Q8, typename Tout>
-cudaError_t launch_d(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, const DeviceCtl &ctl, cudaStream_t s) {
-    if (A.rho == nullptr) return launch_t<D, Q8, false, 1, Tout>(A, p, ws, ctl, s);
-    if (A.pg.group <= 4) return launch_t<D, Q8, true, 1, Tout>(A, p, ws, ctl, s);
-    return launch_t<D, Q8, true, 2, Tout>(A, p, ws, ctl, s);
+cudaError_t launch_d(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, void *mem, const DeviceCtl &ctl,
+                     cudaStream_t s) {
+    if (A.rho == nullptr) return launch_t<D, Q8, false, 1, Tout>(A, sc, mem, ctl, s);
+    if (A.pg.group <= 4) return launch_t<D, Q8, true, 1, Tout>(A, sc, mem, ctl, s);
+    return launch_t<D, Q8, true, 2, Tout>(A, sc, mem, ctl, s);
+}
+
+template <int D, typename Tout>
+cudaError_t launch_q(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, void *mem, const DeviceCtl &ctl,
+                     cudaStream_t s) {
+    return A.kexp ? launch_d<D, true, Tout>(A, sc, mem, ctl, s) : launch_d<D, false, Tout>(A, sc, mem, ctl, s);
 }
 
 }  // namespace
 
-int decode_cache_heads(bool with_rho, int group) { return with_rho ? heads_for<true>(group) : heads_for<false>(group); }
-
-DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, const DecodePlan &p) {
-    const size_t up = 255;
-    const size_t BHS = (size_t)A.B * A.Hq * p.nsplit;
-    const int heads = decode_cache_heads(A.rho != nullptr, A.pg.group);
-    const size_t htiles = (A.pg.group + heads - 1) / heads;
-    DecodeCacheScratch s;
-    s.parts = p.nsplit > 1 ? (BHS * (A.rho ? 2 : 1) * A.d * sizeof(float) + up) & ~up : 0;
-    s.hdr = p.nsplit > 1 || A.wacc ? (BHS * 16 + up) & ~up : 0;
-    s.zs = A.wacc ? (size_t)A.B * A.pg.Hkv * htiles * ((size_t)A.pg.max_pages << A.pg.pshift) * heads * sizeof(float) : 0;
+DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count) {
+    auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    const bool rho = A.rho != nullptr;
+    const int heads = rho ? heads_for<true>(A.pg.group) : heads_for<false>(A.pg.group);
+    const size_t htiles = (A.pg.group + heads - 1) / heads, items = (size_t)A.B * A.pg.Hkv * htiles;
+    const size_t cap = (size_t)A.pg.max_pages << A.pg.pshift;
+    DecodeCacheScratch s{};
+    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (rho && A.pg.group > 4 ? 2 : MINB);
+    s.parts = up((size_t)2 * s.ctas * heads * (rho ? 2 : 1) * A.d * sizeof(float));
+    s.hdr = up((size_t)2 * s.ctas * heads * sizeof(float4));
+    s.cut = up((size_t)s.ctas * sizeof(int2));
+    if (A.wacc) {
+        s.item = up(items * sizeof(int2));
+        s.lse2 = up((size_t)A.B * A.Hq * sizeof(float));
+        s.zs = items * cap * heads * sizeof(float);
+    }
     return s;
 }
 
-cudaError_t launch_decode_cache(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, const DeviceCtl &ctl,
+cudaError_t launch_decode_cache(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, void *mem, const DeviceCtl &ctl,
                                 cudaStream_t s) {
-    const bool f32 = A.out_dtype == PARALLAX_F32;
-    if (A.d == 64) {
-        if (A.kexp)
-            return f32 ? launch_d<64, true, float>(A, p, ws, ctl, s) : launch_d<64, true, __nv_bfloat16>(A, p, ws, ctl, s);
-        return f32 ? launch_d<64, false, float>(A, p, ws, ctl, s) : launch_d<64, false, __nv_bfloat16>(A, p, ws, ctl, s);
-    }
-    if (A.kexp)
-        return f32 ? launch_d<128, true, float>(A, p, ws, ctl, s) : launch_d<128, true, __nv_bfloat16>(A, p, ws, ctl, s);
-    return f32 ? launch_d<128, false, float>(A, p, ws, ctl, s) : launch_d<128, false, __nv_bfloat16>(A, p, ws, ctl, s);
+    if (A.d == 64)
+        return A.out_dtype == PARALLAX_F32 ? launch_q<64, float>(A, sc, mem, ctl, s)
+                                           : launch_q<64, __nv_bfloat16>(A, sc, mem, ctl, s);
+    return A.out_dtype == PARALLAX_F32 ? launch_q<128, float>(A, sc, mem, ctl, s)
+                                       : launch_q<128, __nv_bfloat16>(A, sc, mem, ctl, s);
 }
 
 }  // namespace plx

@@ -51,14 +51,4 @@ inline DecodePlan plan_decode_paged(int B, int Hq, int Hkv, int Tcap, int d, int
     return plan_decode(B, Hkv * ((group + 7) / 8) * 4, Tcap, d, sm_count);
 }
 
-// The cache decode's units (decode_cache.cu) serve up to `heads` query heads of a
-// KV head and are sized like the paged decode's.
-inline DecodePlan plan_decode_cache(int B, int Hq, int Hkv, int heads, int Tcap, int d, int sm_count) {
-    const int group = Hq / Hkv;
-#ifndef UPS
-#define UPS 16
-#endif
-    return plan_decode(B, Hkv * ((group + heads - 1) / heads) * (64 / UPS), Tcap, d, sm_count);
-}
-
 }  // namespace plx

@@ -69,8 +69,11 @@ cudaError_t launch_decode_paged(const void *q, const void *rho, const void *kpag
 // Paged decode over an e4m3 (kexp, vexp set) or bf16 cache, with or without a
 // probe (rho may be null), optionally adding attention weights to wacc
 // [B, Hkv, max_pages << pshift] (decode_cache.cu).
+// tmk, tmv: the pages as {d, page_size, num_pages * Hkv}, boxes of
+// decode_cache_box(d, bf16) elements x 16 rows, swizzled by their row's bytes.
 struct DecodeCacheArgs {
-    const void *q, *rho, *kpages, *vpages;
+    CUtensorMap tmk, tmv;
+    const void *q, *rho;
     const signed char *kexp, *vexp;
     PagedKV pg;
     const int *seqlens;
@@ -78,15 +81,18 @@ struct DecodeCacheArgs {
     float *lse, *wacc;
     int B, Hq, d, out_dtype;
 };
-// Query heads one unit serves.
-int decode_cache_heads(bool with_rho, int group);
-// Scratch of a call in bytes, each part a multiple of 256: split partials, their
-// (m, l, abar) headers, and the scores that the accumulation reads back.
+// elements of a box row: 128 bytes, or the whole row if it is shorter
+inline int decode_cache_box(int d, bool bf16) { return bf16 ? 64 : d; }
+// How a call is cut (decode_sched.h) and its scratch in bytes, each part a multiple
+// of 256: parts of the cut items, their headers, which items are cut, and, with
+// weights, the items' parts, the logs of their sums and the scores.
 struct DecodeCacheScratch {
-    size_t parts, hdr, zs;
+    int ctas;      // 0: one CTA per item
+    size_t parts, hdr, cut, item, lse2, zs;
+    size_t bytes() const { return parts + hdr + cut + item + lse2 + zs; }
 };
-DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, const DecodePlan &p);
-cudaError_t launch_decode_cache(const DecodeCacheArgs &A, const DecodePlan &p, void *ws, const DeviceCtl &ctl,
+DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count);
+cudaError_t launch_decode_cache(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, void *mem, const DeviceCtl &ctl,
                                 cudaStream_t s);
 
 // New tokens into a paged cache (kv_append.cu): k, v [B, Hkv, T, d] bf16 with

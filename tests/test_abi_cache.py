@@ -90,8 +90,9 @@ def test_binding_refuses_before_the_library():
         plx.parallax_kv_evict(codes, codes, table, sl, torch.zeros((1, 2, 32)), table, 16, 0, kexp=e, vexp=e)
 
 
-def test_cache_decode_plan_covers_the_cache(tmp_path):
-    """The split plan of the cache decode covers every token and stays within the launch limits."""
+def test_cache_decode_schedule(tmp_path):
+    """Every quad of every item belongs to one CTA's range, ranges are even, and the parts of a cut item are
+    found where their CTAs left them."""
     import os
     import shutil
     import subprocess
@@ -100,25 +101,52 @@ def test_cache_decode_plan_covers_the_cache(tmp_path):
     if gxx is None:
         pytest.skip("no g++")
     csrc = os.path.join(os.path.dirname(plx.__file__), "csrc")
-    src = tmp_path / "plan.cpp"
+    src = tmp_path / "sched.cpp"
     src.write_text(r"""
 #include <cstdio>
-#include "decode_plan.h"
+#include <cstdlib>
+#include <vector>
+#include "decode_sched.h"
+using namespace plx;
 int main() {
-    for (int B = 1; B <= 4096; B = B * 3 + 1)
-        for (int Hkv = 1; Hkv <= 64; Hkv *= 2)
-            for (int G = 1; G <= 24; G += 5)
-                for (int heads = 4; heads <= 8; heads += 4)
-                    for (long T = 16; T <= (1 << 20); T = T * 5 + 16) {
-                        const long cap = T / 16 * 16;
-                        const plx::DecodePlan p = plx::plan_decode_cache(B, Hkv * G, Hkv, heads, (int)cap, 128, 148);
-                        const long units = (long)B * Hkv * ((G + heads - 1) / heads);
-                        if ((long)p.chunk * p.nsplit < cap || p.chunk % 16 != 0 || p.nsplit < 1) return 1;
-                        if (p.nsplit > 1 && units * p.nsplit > 64L * 148) return 2;
-                    }
-    return 0;
+    srand(1);
+    for (int rep = 0; rep < 400; ++rep) {
+        const int ctas = 1 + rand() % 700, items = 1 + rand() % 300;
+        std::vector<long long> first(1, 0);
+        for (int i = 0; i < items; ++i) first.push_back(first.back() + (rand() % 3 ? rand() % (rep % 50 + 1) : 0));
+        const long long total = first.back();
+        if (total == 0) continue;
+        const int n = sched_ctas(total, ctas);
+        if (n < 1 || n > ctas) return 1;
+        std::vector<int> who(total, -1);
+        for (int c = 0; c < n; ++c) {
+            const long long a = sched_start(c, total, n), b = sched_start(c + 1, total, n);
+            if (b <= a || b - a > total / n + 1) return 2;
+            for (long long x = a; x < b; ++x) {
+                if (who[x] != -1 || sched_owner(x, total, n) != c) return 3;
+                who[x] = c;
+            }
+        }
+        std::vector<int> slot_item(2 * n, -1);
+        for (int i = 0; i < items; ++i) {
+            if (first[i] == first[i + 1]) continue;
+            const int c0 = who[first[i]], c1 = who[first[i + 1] - 1];
+            const int parts = sched_owner(first[i + 1] - 1, total, n) - c0 + 1;
+            if (parts != c1 - c0 + 1) return 4;
+            if (parts == 1) continue;
+            for (int c = c0; c <= c1; ++c) {
+                const int slot = sched_slot(c, c == c0);      // as the CTA writes it
+                if (slot != sched_part(c0, c - c0)) return 5;  // as the merge reads it
+                if (slot < 0 || slot >= 2 * n || slot_item[slot] != -1) return 6;
+                slot_item[slot] = i;
+            }
+        }
+    }
+    // the largest batches stay within 64 bits
+    const long long total = (1ll << 36) / QUAD;
+    return sched_owner(total - 1, total, 592) == 591 && sched_start(592, total, 592) == total ? 0 : 7;
 }
 """)
-    exe = tmp_path / "plan"
+    exe = tmp_path / "sched"
     subprocess.check_call([gxx, "-O1", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)])
     assert subprocess.call([str(exe)]) == 0

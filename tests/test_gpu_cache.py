@@ -282,13 +282,20 @@ def test_decode_split_over_a_long_cache(with_rho, q8):
     assert torch.equal(y, y2) and torch.equal(lse, lse2) and torch.equal(w, w2)     # no schedule in the result
 
 
-def test_decode_one_split_and_bf16_output():
-    """A batch so large that no sequence is split."""
+def test_decode_many_sequences_and_bf16_output():
+    """More items than CTAs, in short tables (a CTA per item) and in long ones that the lengths do not fill."""
     rng = np.random.default_rng(9)
     c = Cache(rng, 300, 16, 16, 2, 64)
     q, rho = (bf16(rng.standard_normal((300, 16, 64))) for _ in range(2))
     check_decode(c, q, rho, list(rng.integers(0, 33, 300)), out_dtype=torch.bfloat16)
     check_decode(c, q, rho, list(rng.integers(0, 33, 300)), with_acc=False)
+    c = Cache(rng, 150, 3, 16, 25, 64)
+    q, rho = (bf16(rng.standard_normal((150, 3 * 9, 64))) for _ in range(2))
+    sl = rng.integers(0, 400, 150)
+    sl[:40] = sl[-7:] = 0
+    check_decode(c, q, rho, list(sl), out_dtype=torch.bfloat16)
+    check_decode(c, q, None, list(rng.integers(0, 3, 150)))
+    check_decode(c, q, None, [0] * 150)
 
 
 def test_decode_with_heavy_and_light_blocks():
