@@ -49,15 +49,6 @@ namespace plx {
 namespace {
 
 constexpr int WARPS = 4;
-#ifndef Q8_STAGES
-#define Q8_STAGES 3
-#endif
-#ifndef BF_STAGES
-#define BF_STAGES 3
-#endif
-#ifndef MINB
-#define MINB 4
-#endif
 // Tables of at most this many tokens: one CTA per item, no merge.
 constexpr int WHOLE_TOKENS = 256;
 constexpr float MNONE = -1e30f;     // reference of a row that has seen no score
@@ -155,7 +146,11 @@ template <int D, bool Q8, bool RHO, int NT> struct Shape {
     static constexpr int BOXES = ROW / RB;               // boxes of a K or V tile
     static constexpr int HALF = 16 * ROW;                // bytes of a K or V tile
     static constexpr int TILE_BYTES = 2 * HALF;
-    static constexpr int STAGES = Q8 ? Q8_STAGES : BF_STAGES;            // tiles in flight per warp: STAGES - 1
+    static constexpr int STAGES = TILE_BYTES <= 2048 ? 4 : 2;            // tiles of a warp's ring
+    // CTAs per SM that registers (128, 168 and 255 a thread) and rings leave room for;
+    // d = 128, e4m3: 4 CTAs of 2 stages against 3 of 4: 256 against 267 us (B=16, 16
+    // heads, 32768 tokens); bf16: 3 of 2 against 4 of 1 or 2 of 3 (160 us each).
+    static constexpr int CTAS = NT == 2 ? 2 : (Q8 || D == 64 ? 4 : 3);
     static constexpr int RING_BYTES = WARPS * STAGES * TILE_BYTES;
     static constexpr int BAR_OFF = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
     static constexpr int SMEM = BAR_OFF + 8 * WARPS * STAGES + 1024;     // and what aligning the base to 1024 takes
@@ -169,13 +164,13 @@ struct Scratch {
     float *parts;       // [slot][HEADS][O, M]
     float4 *hdr;        // [slot][HEADS] (m, l, abar) of the cut items' parts
     int2 *cut;          // [CTA] (item, parts) of the item it starts but does not finish, or (-1, 0)
-    int2 *item;         // [item] (first CTA, parts), with weights
+    int2 *item;         // [item] (first CTA, parts)
     float *lse2;        // [B, Hq] log2 of an uncut item's sum, with weights
     float *zs;          // [item][Tcap][HEADS] scores (log2), with weights
 };
 
 template <int D, bool Q8, bool RHO, int NT, typename Tout>
-__global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cache(
+__global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_decode_cache(
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
     const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ rho, const signed char *__restrict__ kexp,
     const signed char *__restrict__ vexp, const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse,
@@ -196,6 +191,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
     const int per_seq = pg.Hkv * htiles;     // items of a sequence
     auto len_of = [&](int i) { return min(max(seqlens[i], 0), Tcap); };
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- this CTA's range of quads: from quad `q0` of item `it` of sequence `b`, `left` quads ----
     int b, it, q0 = 0, cta = 0, nctas = 1;
     long long left, pos = 0, total = 1;
@@ -278,57 +274,6 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
         const int ntiles = (t1 - t0 + 15) / 16;
         const bool uncut = q0 == 0 && q1 == nq;
 
-        // ---- the vectors: column n = r of n-tile nt; 4 elements per MMA step ----
-        uint32_t qf[NT][S::KSTEPS][2];
-        float zfac[S::HPT], afac[S::HPT];    // of the heads whose state this thread holds
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int head = RHO ? nt * 4 + r / 2 : nt * 8 + r;
-            const bool live = head < nh;
-            const __nv_bfloat16 *src = (RHO && (r & 1) ? rho : q) + (h0 + (live ? head : 0)) * D;
-            uint2 w[S::KSTEPS];
-            uint32_t big = 0;
-#pragma unroll
-            for (int s = 0; s < S::KSTEPS; ++s) {
-                const int d0 = Q8 ? 64 * (s / 4) + 16 * t4 + 4 * (s % 4) : 32 * (s / 2) + 8 * t4 + 4 * (s % 2);
-                w[s] = live ? *reinterpret_cast<const uint2 *>(src + d0) : make_uint2(0u, 0u);
-                big = max(big, max(max(w[s].x & 0x7fffu, w[s].x >> 16 & 0x7fffu), max(w[s].y & 0x7fffu, w[s].y >> 16 & 0x7fffu)));
-            }
-            float inv = 1.f;
-            if constexpr (Q8) {
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                // bring the largest element to [2^7, 2^8)
-                const int up = min(max(134 - (int)(big >> 7), -110), 110);
-                const float f = exp2_whole(up);
-                inv = exp2_whole(-up);
-#pragma unroll
-                for (int s = 0; s < S::KSTEPS; ++s) {
-                    const __half2 a = __floats2half2_rn(__uint_as_float(w[s].x << 16) * f,
-                                                        __uint_as_float(w[s].x & 0xffff0000u) * f);
-                    const __half2 c = __floats2half2_rn(__uint_as_float(w[s].y << 16) * f,
-                                                        __uint_as_float(w[s].y & 0xffff0000u) * f);
-                    qf[nt][s][0] = *reinterpret_cast<const uint32_t *>(&a);
-                    qf[nt][s][1] = *reinterpret_cast<const uint32_t *>(&c);
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < S::KSTEPS; ++s) {
-                    qf[nt][s][0] = w[s].x;
-                    qf[nt][s][1] = w[s].y;
-                }
-            }
-            // columns 2 t4 and 2 t4 + 1 of the score product: (z, a) of one head, or z of two
-            const float f0 = __shfl_sync(0xffffffffu, inv, 8 * t4), f1 = __shfl_sync(0xffffffffu, inv, 8 * t4 + 4);
-            if constexpr (RHO) {
-                zfac[nt] = f0 * scale_log2;
-                afac[nt] = f1;
-            } else {
-                zfac[2 * nt] = f0 * scale_log2;
-                zfac[2 * nt + 1] = f1 * scale_log2;
-            }
-        }
-
         float oacc[NT][S::JS][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -387,6 +332,57 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
             const int id = __shfl_sync(0xffffffffu, ids, j);
             if (j < mine) issue(j, (stage + j) % S::STAGES, id);
         }
+        // ---- the vectors (the first tiles are on their way): column n = r of n-tile nt; 4 elements per MMA step ----
+        uint32_t qf[NT][S::KSTEPS][2];
+        float zfac[S::HPT], afac[S::HPT];    // of the heads whose state this thread holds
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int head = RHO ? nt * 4 + r / 2 : nt * 8 + r;
+            const bool live = head < nh;
+            const __nv_bfloat16 *src = (RHO && (r & 1) ? rho : q) + (h0 + (live ? head : 0)) * D;
+            uint2 w[S::KSTEPS];
+            uint32_t big = 0;
+#pragma unroll
+            for (int s = 0; s < S::KSTEPS; ++s) {
+                const int d0 = Q8 ? 64 * (s / 4) + 16 * t4 + 4 * (s % 4) : 32 * (s / 2) + 8 * t4 + 4 * (s % 2);
+                w[s] = live ? *reinterpret_cast<const uint2 *>(src + d0) : make_uint2(0u, 0u);
+                big = max(big, max(max(w[s].x & 0x7fffu, w[s].x >> 16 & 0x7fffu), max(w[s].y & 0x7fffu, w[s].y >> 16 & 0x7fffu)));
+            }
+            float inv = 1.f;
+            if constexpr (Q8) {
+                big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                // bring the largest element to [2^7, 2^8)
+                const int up = min(max(134 - (int)(big >> 7), -110), 110);
+                const float f = exp2_whole(up);
+                inv = exp2_whole(-up);
+#pragma unroll
+                for (int s = 0; s < S::KSTEPS; ++s) {
+                    const __half2 a = __floats2half2_rn(__uint_as_float(w[s].x << 16) * f,
+                                                        __uint_as_float(w[s].x & 0xffff0000u) * f);
+                    const __half2 c = __floats2half2_rn(__uint_as_float(w[s].y << 16) * f,
+                                                        __uint_as_float(w[s].y & 0xffff0000u) * f);
+                    qf[nt][s][0] = *reinterpret_cast<const uint32_t *>(&a);
+                    qf[nt][s][1] = *reinterpret_cast<const uint32_t *>(&c);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < S::KSTEPS; ++s) {
+                    qf[nt][s][0] = w[s].x;
+                    qf[nt][s][1] = w[s].y;
+                }
+            }
+            // columns 2 t4 and 2 t4 + 1 of the score product: (z, a) of one head, or z of two
+            const float f0 = __shfl_sync(0xffffffffu, inv, 8 * t4), f1 = __shfl_sync(0xffffffffu, inv, 8 * t4 + 4);
+            if constexpr (RHO) {
+                zfac[nt] = f0 * scale_log2;
+                afac[nt] = f1;
+            } else {
+                zfac[2 * nt] = f0 * scale_log2;
+                zfac[2 * nt + 1] = f1 * scale_log2;
+            }
+        }
+
         // where this thread's tokens and chunks lie in a tile
         const int tok0 = row_of<S::RB>(r), tok1 = tok0 + 8;
         const int koff = chunk_at<S::RB>(tok0, t4);
@@ -697,121 +693,142 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? MINB : 2)) k_decode_cac
     }
 }
 
-// One launch after the decode: the first blocks, HEADS per CTA of the decode, merge
-// the parts of the item that CTA starts but does not finish (one head each) and
-// write y and lse; the others add the weights s = 2^(z - lse2) of ACC_TOKENS
-// tokens of one (b, kvh) to the accumulator, summed over the KV head's query
-// heads in head order (each token by one thread: the result does not depend on
-// the schedule).
+// One launch after the decode (a programmatic dependent: its blocks are there when
+// the decode's CTAs leave).  The first blocks merge cut items and write y and lse:
+// one per CTA of the decode (the item that CTA starts but does not finish) with all
+// its heads, or, when items are few and have many parts (hpb = 1), one per item
+// and head; the others add the weights s = 2^(z - lse2) of ACC_TOKENS tokens of
+// one (b, kvh) to the accumulator, summed over the KV head's query heads in head
+// order (each token by one thread: the result does not depend on the schedule).
 constexpr int FIN_THREADS = 256;
 constexpr int ACC_TOKENS = 1024;
 
 template <int D, bool RHO, int HEADS, typename Tout>
 __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
     Scratch ws, const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse, float *__restrict__ wacc,
-    int Hq, int Hkv, int htiles, int Tcap, int ctas, int combine_blocks, int acc_chunks) {
+    int Hq, int Hkv, int htiles, int Tcap, int ctas, int hpb, int combine_blocks, int acc_chunks) {
     constexpr int COLS = (RHO ? 2 : 1) * D / 4;               // float4 columns of a part
-    constexpr int GROUPS = FIN_THREADS / COLS;                // parts in flight
+    constexpr int GROUPS = FIN_THREADS / COLS;                // thread groups of one column each
     __shared__ float4 red[GROUPS][COLS];
     __shared__ float2 redl[GROUPS];
-    __shared__ float wred[FIN_THREADS / 32];
     __shared__ float slse[HEADS];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int group = Hq / Hkv;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x < combine_blocks) {
-        const int c0 = blockIdx.x / HEADS, hh = blockIdx.x % HEADS;
-        const int2 cut = ws.cut[c0];
-        if (cut.x < 0) return;
-        const int per_seq = Hkv * htiles, b = cut.x / per_seq, it = cut.x % per_seq;
-        const int g = (it % htiles) * HEADS + hh;
-        if (g >= group) return;
-        const long bh = (long)b * Hq + (long)(it / htiles) * group + g;
-        const int nv = cut.y;
-        float mu = -INFINITY;
-        for (int s = tid; s < nv; s += FIN_THREADS) mu = fmaxf(mu, ws.hdr[sched_part(c0, s) * HEADS + hh].x);
-#pragma unroll
-        for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
-        if (lane == 0) wred[warp] = mu;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < FIN_THREADS / 32; ++w) mu = fmaxf(mu, wred[w]);
+        const int at = blockIdx.x / (HEADS / hpb), hfirst = blockIdx.x % (HEADS / hpb) * hpb;
+        const int per_seq = Hkv * htiles;
+        int item, c0, nv;                                     // the cut item, its first CTA and its parts
+        if (hpb == 1) {
+            const int2 info = ws.item[at];
+            item = at;
+            c0 = info.x;
+            nv = info.y;
+            // not written: an empty sequence, or a decode that gave up on a wait
+            if (seqlens[at / per_seq] <= 0 || c0 < 0 || c0 >= ctas || nv < 2 || nv > ctas - c0) return;
+        } else {
+            const int2 cut = ws.cut[at];
+            item = cut.x;
+            c0 = at;
+            nv = cut.y;
+            if (item < 0) return;
+        }
+        const int b = item / per_seq, it = item % per_seq;
+        const int g0 = (it % htiles) * HEADS;
+        const long bh0 = (long)b * Hq + (long)(it / htiles) * group + g0;
         const int col = tid % COLS, grp = tid / COLS;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f, ab = 0.f;
-        const float4 *P = reinterpret_cast<const float4 *>(ws.parts) + col;
+        // `by` groups share a head's parts: all of them when a block has one head, else one each
+        const int by = hpb == 1 ? GROUPS : 1, heads = GROUPS / by;
+        for (int h1 = hfirst; h1 < hfirst + hpb; h1 += heads) {
+            const int hh = h1 + grp / by;
+            const bool live = hh < hfirst + hpb && g0 + hh < group;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f, ab = 0.f, mu = MNONE;
+            if (live) {                                       // a group is whole warps, so is `live`
+                for (int s = lane; s < nv; s += 32) mu = fmaxf(mu, ws.hdr[sched_part(c0, s) * HEADS + hh].x);
+#pragma unroll
+                for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
+                const float4 *P = reinterpret_cast<const float4 *>(ws.parts) + col;
 #pragma unroll 4
-        for (int s = grp; s < nv; s += GROUPS) {
-            const int slot = sched_part(c0, s) * HEADS + hh;
-            const float4 h = ws.hdr[slot];
-            const float4 p = P[(size_t)slot * COLS];
-            const float w = fex2(h.x - mu);
-            l = fmaf(w, h.y, l);
-            ab = fmaf(w, h.z, ab);
-            acc.x = fmaf(w, p.x, acc.x);
-            acc.y = fmaf(w, p.y, acc.y);
-            acc.z = fmaf(w, p.z, acc.z);
-            acc.w = fmaf(w, p.w, acc.w);
-        }
-        red[grp][col] = acc;
-        if (col == 0) redl[grp] = make_float2(l, ab);
-        __syncthreads();
-        l = ab = 0.f;
-#pragma unroll
-        for (int i = 0; i < GROUPS; ++i) {
-            l += redl[i].x;
-            ab += redl[i].y;
-        }
-        const float inv = 1.f / l;
-        const float *R = reinterpret_cast<const float *>(red);
-        for (int e = tid; e < D; e += FIN_THREADS) {
-            float o = 0.f, m = 0.f;
-#pragma unroll
-            for (int i = 0; i < GROUPS; ++i) {
-                o += R[i * COLS * 4 + e];
-                if constexpr (RHO) m += R[i * COLS * 4 + D + e];
+                for (int s = grp % by; s < nv; s += by) {
+                    const int slot = sched_part(c0, s) * HEADS + hh;
+                    const float4 h = ws.hdr[slot];
+                    const float4 p = P[(size_t)slot * COLS];
+                    const float w = fex2(h.x - mu);
+                    l = fmaf(w, h.y, l);
+                    ab = fmaf(w, h.z, ab);
+                    acc.x = fmaf(w, p.x, acc.x);
+                    acc.y = fmaf(w, p.y, acc.y);
+                    acc.z = fmaf(w, p.z, acc.z);
+                    acc.w = fmaf(w, p.w, acc.w);
+                }
             }
-            float out = o * inv;
-            if constexpr (RHO) out -= m * inv - out * (ab * inv);
-            store_y<Tout>(y + bh * D + e, out);
+            __syncthreads();
+            red[grp][col] = acc;
+            if (col == 0) redl[grp] = make_float2(l, ab);
+            __syncthreads();
+            if (live) {
+                const int first = grp / by * by;              // the groups of this head
+                l = ab = 0.f;
+                for (int i = 0; i < by; ++i) {
+                    l += redl[first + i].x;
+                    ab += redl[first + i].y;
+                }
+                const float inv = 1.f / l;
+                const float *R = reinterpret_cast<const float *>(red[first]);
+                for (int e = tid - first * COLS; e < D; e += by * COLS) {
+                    float o = 0.f, m = 0.f;
+                    for (int i = 0; i < by; ++i) {
+                        o += R[i * COLS * 4 + e];
+                        if constexpr (RHO) m += R[i * COLS * 4 + D + e];
+                    }
+                    float out = o * inv;
+                    if constexpr (RHO) out -= m * inv - out * (ab * inv);
+                    store_y<Tout>(y + (bh0 + hh) * D + e, out);
+                    if (e == 0 && lse != nullptr) lse[bh0 + hh] = (mu + log2f(l)) * LN2;
+                }
+            }
         }
-        if (lse != nullptr && tid == 0) lse[bh] = (mu + log2f(l)) * LN2;
         return;
     }
-    // ---- accumulate ----
-    const long rest = (long)blockIdx.x - combine_blocks;
-    const int ck = (int)(rest % acc_chunks);
-    const long bk = rest / acc_chunks;                         // b * Hkv + kvh
-    const int b = (int)(bk / Hkv), kvh = (int)(bk % Hkv);
-    const int L = min(max(seqlens[b], 0), Tcap);
-    const int t0 = ck * ACC_TOKENS;
-    if (t0 >= L) return;
+    // ---- accumulate: every load whose address is known is issued first ----
+    const unsigned rest = blockIdx.x - combine_blocks;
+    const int t0 = (int)(rest % (unsigned)acc_chunks) * ACC_TOKENS;
+    const unsigned bk = rest / (unsigned)acc_chunks;           // b * Hkv + kvh
+    const int b = (int)(bk / (unsigned)Hkv), kvh = (int)(bk % (unsigned)Hkv);
     constexpr int PER = ACC_TOKENS / FIN_THREADS;
-    float sum[PER];
+    const int L = min(max(seqlens[b], 0), Tcap);
+    float sum[PER], had[PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) sum[k] = 0.f;
+    for (int k = 0; k < PER; ++k) {
+        const int t = t0 + tid + k * FIN_THREADS;
+        sum[k] = 0.f;
+        had[k] = t < Tcap ? wacc[(size_t)bk * Tcap + t] : 0.f;
+    }
     for (int ht = 0; ht < htiles; ++ht) {
         const int nh = min(HEADS, group - ht * HEADS);
-        const long item = bk * htiles + ht;
-        // the scores do not wait for the sums
+        const int item = (int)bk * htiles + ht;
+        const long h0 = (long)b * Hq + (long)kvh * group + ht * HEADS;
         float4 z[PER][HEADS / 4];
 #pragma unroll
         for (int k = 0; k < PER; ++k)
 #pragma unroll
             for (int c = 0; c < HEADS / 4; ++c) {
                 const int t = t0 + tid + k * FIN_THREADS;
-                z[k][c] = t < L ? reinterpret_cast<const float4 *>(ws.zs + ((size_t)item * Tcap + t) * HEADS)[c]
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                z[k][c] = t < Tcap ? reinterpret_cast<const float4 *>(ws.zs + ((size_t)item * Tcap + t) * HEADS)[c]
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         int2 info = ws.item[item];
+        float l2 = lane < nh ? ws.lse2[h0 + lane] : 0.f;       // of an uncut item
+        if (t0 >= L) return;
         // a decode that gave up on a wait has not written it: whatever is read stays in bounds
-        if (info.y != 1 && (info.x < 0 || info.x >= ctas || info.y < 1 || info.y > ctas - info.x)) info = make_int2(0, 1);
+        if (info.x < 0 || info.x >= ctas || info.y < 1 || info.y > ctas - info.x) info = make_int2(0, 1);
         __syncthreads();
-        for (int h = warp; h < nh; h += FIN_THREADS / 32) {
-            float l2;
-            if (info.y == 1) {
-                l2 = ws.lse2[(long)b * Hq + (long)kvh * group + ht * HEADS + h];
-            } else {
-                float mu = -INFINITY, l = 0.f;
+        if (info.y == 1) {
+            if (tid < nh) slse[tid] = l2;
+        } else {
+            for (int h = warp; h < nh; h += FIN_THREADS / 32) {
+                float mu = MNONE, l = 0.f;
                 for (int s = lane; s < info.y; s += 32) mu = fmaxf(mu, ws.hdr[sched_part(info.x, s) * HEADS + h].x);
 #pragma unroll
                 for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
@@ -821,9 +838,8 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
                 }
 #pragma unroll
                 for (int off = 16; off > 0; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
-                l2 = mu + log2f(l);
+                if (lane == 0) slse[h] = mu + log2f(l);
             }
-            if (lane == 0) slse[h] = l2;
         }
         __syncthreads();
 #pragma unroll
@@ -839,12 +855,9 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int t = t0 + tid + k * FIN_THREADS;
-        if (t < L) wacc[(size_t)bk * Tcap + t] += sum[k];
+        if (t < L) wacc[(size_t)bk * Tcap + t] = had[k] + sum[k];
     }
 }
-
-// heads of a unit for a group of query heads
-template <bool RHO> int heads_for(int group) { return RHO ? (group <= 4 ? 4 : 8) : 8; }
 
 template <int D, bool Q8, bool RHO, int NT, typename Tout>
 cudaError_t launch_t(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, void *mem, const DeviceCtl &ctl,
@@ -873,12 +886,22 @@ cudaError_t launch_t(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, voi
         A.tmk, A.tmv, (const __nv_bfloat16 *)A.q, (const __nv_bfloat16 *)A.rho, A.kexp, A.vexp, A.seqlens, (Tout *)A.y, A.lse, A.B, A.Hq, htiles, whole, A.pg, ws, ctl);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (whole && A.wacc == nullptr)) return e;
-    const int combine = whole ? 0 : grid * S::HEADS;
+    // few items have many parts each and take a block per head, many items have two or three
+    const int items = A.B * A.pg.Hkv * htiles;
+    const int hpb = items >= 128 ? S::HEADS : 1;
+    const int combine = whole ? 0 : (hpb == 1 ? items * S::HEADS : grid);
     const int acc_chunks = A.wacc ? (Tcap + ACC_TOKENS - 1) / ACC_TOKENS : 0;
-    const long blocks = combine + (long)A.B * A.pg.Hkv * acc_chunks;
-    k_decode_finish<D, RHO, S::HEADS, Tout><<<(unsigned)blocks, FIN_THREADS, 0, s>>>(
-        ws, A.seqlens, (Tout *)A.y, A.lse, A.wacc, A.Hq, A.pg.Hkv, htiles, Tcap, sc.ctas, combine, acc_chunks);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(combine + (long)A.B * A.pg.Hkv * acc_chunks));
+    cfg.blockDim = dim3(FIN_THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_decode_finish<D, RHO, S::HEADS, Tout>, ws, A.seqlens, (Tout *)A.y, A.lse, A.wacc,
+                              A.Hq, A.pg.Hkv, htiles, Tcap, whole ? 1 : sc.ctas, hpb, combine, acc_chunks);
 }
 
 template <int D, bool Q8, typename Tout>
@@ -899,17 +922,17 @@ cudaError_t launch_q(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, voi
 
 DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count) {
     auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
-    const bool rho = A.rho != nullptr;
-    const int heads = rho ? heads_for<true>(A.pg.group) : heads_for<false>(A.pg.group);
+    const bool rho = A.rho != nullptr, q8 = A.kexp != nullptr;
+    const int heads = rho && A.pg.group <= 4 ? 4 : 8;
     const size_t htiles = (A.pg.group + heads - 1) / heads, items = (size_t)A.B * A.pg.Hkv * htiles;
     const size_t cap = (size_t)A.pg.max_pages << A.pg.pshift;
     DecodeCacheScratch s{};
-    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (rho && A.pg.group > 4 ? 2 : MINB);
+    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (rho && A.pg.group > 4 ? 2 : (q8 || A.d == 64 ? 4 : 3));
     s.parts = up((size_t)2 * s.ctas * heads * (rho ? 2 : 1) * A.d * sizeof(float));
     s.hdr = up((size_t)2 * s.ctas * heads * sizeof(float4));
     s.cut = up((size_t)s.ctas * sizeof(int2));
+    s.item = s.ctas || A.wacc ? up(items * sizeof(int2)) : 0;
     if (A.wacc) {
-        s.item = up(items * sizeof(int2));
         s.lse2 = up((size_t)A.B * A.Hq * sizeof(float));
         s.zs = items * cap * heads * sizeof(float);
     }
