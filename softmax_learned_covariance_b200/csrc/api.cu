@@ -576,7 +576,7 @@ int parallax_kv_evict(void *kpages, void *vpages, signed char *kexp, signed char
     if (st) return st;
     if ((st = paged_layout(block_table, B, Hkv, page_size, max_pages, num_pages, d, &A.pg))) return st;
     if (budget < 1 || recent < 0 || recent > budget || budget > (long long)new_max_pages * page_size ||
-        (long long)B * Hkv > (1ll << 30))
+        (long long)B * Hkv > (1ll << 28) || (__int128)B * Hkv * budget > ((__int128)1 << 34))
         return PARALLAX_ERR_SHAPE;
     if ((st = cache_dtype_ok(cache_dtype, kexp, vexp))) return st;
     if (!aligned16(kpages) || !aligned16(vpages) || !aligned4(block_table) || !aligned4(seqlens) || !aligned16(wacc) ||
@@ -586,7 +586,7 @@ int parallax_kv_evict(void *kpages, void *vpages, signed char *kexp, signed char
     if (new_table == block_table || new_seqlens == seqlens || new_wacc == wacc) return PARALLAX_ERR_UNSUPPORTED;
     DevState *s = nullptr;
     if ((st = get_state(&s))) return st;
-    return status_of(launch_kv_evict(A, make_ctl(s), static_cast<cudaStream_t>(stream)));
+    return status_of(launch_kv_evict(A, s->sms, make_ctl(s), static_cast<cudaStream_t>(stream)));
 }
 
 int parallax_decode_ex(const void *q, const void *rho, const void *kcache, const void *vcache, const int *seqlens,

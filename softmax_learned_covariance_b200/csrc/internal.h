@@ -123,7 +123,7 @@ struct KvEvictArgs {
     float *new_wacc;
     int B, d, budget, recent, new_max_pages;
 };
-cudaError_t launch_kv_evict(const KvEvictArgs &A, const DeviceCtl &ctl, cudaStream_t s);
+cudaError_t launch_kv_evict(const KvEvictArgs &A, int sm_count, const DeviceCtl &ctl, cudaStream_t s);
 
 // Wait policy and test hooks from the environment (PARALLAX_WAIT_TIMEOUT_MS,
 // PARALLAX_DEBUG_FLAGS) around the given device error word.  No allocation.

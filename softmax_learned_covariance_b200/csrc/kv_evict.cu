@@ -7,18 +7,25 @@
 // are only read.
 //
 // Two launches.  k_evict_select finds the weight of the last kept token by a
-// radix select over order-preserving integer keys and writes the kept
-// positions in order; k_evict_move copies the rows, one warp per 16-row
-// destination block.  An e4m3 destination block takes the largest exponent of
-// its rows' source blocks and the rows of smaller ones are moved to it (exact
-// until subnormal).
+// radix select over order-preserving integer keys (three digits of 11, 11 and 10
+// bits) and writes the kept positions in order: a cluster of CTAs per head, whose
+// histograms meet in distributed shared memory; a CTA whose share is at most
+// SEL_TILE tokens reads its weights once and keeps the keys in registers.
+// k_evict_move copies the rows, one warp per 16-row destination block.  An e4m3
+// destination block takes the largest exponent of its rows' source blocks and the
+// rows of smaller ones are moved to it (exact until subnormal).
+#include <cooperative_groups.h>
+
 #include "cache_common.cuh"
 
 namespace plx {
 namespace {
 
-constexpr int SEL_THREADS = 1024;
+constexpr int SEL_THREADS = 512;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int SEL_ITEMS = 8;                            // tokens of a thread at a time
+constexpr int SEL_TILE = SEL_THREADS * SEL_ITEMS;
+constexpr int BINS = 2048;
 constexpr int MOVE_WARPS = 4;
 
 // Weights as integers in the same order: -0 and +0 are equal, NaN is -inf.
@@ -52,81 +59,150 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *wsum, uint3
     return x - v + (warp > 0 ? before : 0u);
 }
 
-__global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A) {
-    __shared__ uint32_t hist[2048];
+__global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A, int cluster_size) {
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    __shared__ __align__(16) uint32_t hist[3][BINS];
     __shared__ uint32_t wsum[32];
-    __shared__ uint32_t pick, above;
-    const int tid = threadIdx.x;
-    const long bk = blockIdx.x;
+    __shared__ uint32_t pick, above, mine[2];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, rank = blockIdx.x % cluster_size;
+    const long bk = blockIdx.x / cluster_size;
     const int b = (int)(bk / A.pg.Hkv);
     const int cap = A.pg.max_pages << A.pg.pshift;
     const size_t ncap = (size_t)A.new_max_pages << A.pg.pshift;
     const int L = min(max(A.seqlens[b], 0), cap);
     const int n = min(L, A.budget), tail = min(A.recent, n);
     const int C = L - tail, need = n - tail;           // `need` of the first C, then the last `tail`
-    if (bk % A.pg.Hkv == 0 && tid == 0) A.new_seqlens[b] = n;
+    if (bk % A.pg.Hkv == 0 && rank == 0 && tid == 0) A.new_seqlens[b] = n;
     const float *w = A.wacc + (size_t)bk * cap;
     int *kept = A.kept + (size_t)bk * A.budget;
     float *nw = A.new_wacc ? A.new_wacc + bk * ncap : nullptr;
+    for (int i = rank * SEL_THREADS + tid; i < tail; i += cluster_size * SEL_THREADS) {
+        kept[need + i] = C + i;
+        if (nw) nw[need + i] = w[C + i];
+    }
+    if (need == 0) return;                             // the whole cluster
+    // this CTA's candidates [begin, end)
+    const int share = ((C + cluster_size - 1) / cluster_size + 3) & ~3;
+    const int begin = min(rank * share, C), end = min(begin + share, C);
+    const bool all = need == C, once = share <= SEL_TILE;
 
+    float x[SEL_ITEMS];
+    auto load = [&](int base) {                        // tokens base + 8 tid ..; past `end`: not looked at
+#pragma unroll
+        for (int v = 0; v < SEL_ITEMS; v += 4) {
+            const int t = base + SEL_ITEMS * tid + v;
+            const float4 f = t < end ? *reinterpret_cast<const float4 *>(w + t) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[v] = f.x;
+            x[v + 1] = f.y;
+            x[v + 2] = f.z;
+            x[v + 3] = f.w;
+        }
+    };
+    if (once) load(begin);
     uint32_t prefix = 0, mask = 0, ties = 0;           // the need-th largest key, found from the top bits down
-    if (need > 0 && need < C) {
+    if (!all) {
+        for (int i = tid; i < 3 * BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0u;
+        __syncthreads();
         uint32_t left = (uint32_t)need;                // how many of the keys that match `prefix` are wanted
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-            const int bits = pass == 2 ? 10 : 11;
-            for (int i = tid; i < 2048; i += SEL_THREADS) hist[i] = 0u;
-            __syncthreads();
-            for (int t = tid; t < C; t += SEL_THREADS) {
-                const uint32_t k = order_key(w[t]);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+            const uint32_t digit = pass == 2 ? 1023u : 2047u;
+            for (int base = begin; base < end; base += SEL_TILE) {
+                if (!once) load(base);
+#pragma unroll
+                for (int i = 0; i < SEL_ITEMS; ++i) {
+                    const uint32_t k = order_key(x[i]);
+                    if (base + SEL_ITEMS * tid + i < end && (k & mask) == prefix)
+                        atomicAdd(&hist[pass][(k >> shift) & digit], 1u);
+                }
             }
-            __syncthreads();
-            // thread i owns the bins 2047 - 2i and 2046 - 2i: an exclusive sum from the largest bin down
-            const uint32_t h0 = hist[2047 - 2 * tid], h1 = hist[2046 - 2 * tid];
+            cluster.sync();                            // every CTA's histogram of this digit is complete
+            // thread i owns bins 2047 - 4 i .. 2044 - 4 i: an exclusive sum from the largest bin down
+            uint4 h = make_uint4(0u, 0u, 0u, 0u);
+            for (int q = 0; q < cluster_size; ++q) {
+                const uint32_t *theirs = cluster.map_shared_rank(&hist[pass][0], q);
+                const uint4 o = *reinterpret_cast<const uint4 *>(theirs + BINS - 4 - 4 * tid);
+                h.x += o.x;
+                h.y += o.y;
+                h.z += o.z;
+                h.w += o.w;
+            }
             uint32_t total;
-            const uint32_t before = block_scan(h0 + h1, wsum, total);
-            if (before < left && left <= before + h0 + h1) {
-                const bool first = left <= before + h0;
-                pick = (uint32_t)(first ? 2047 - 2 * tid : 2046 - 2 * tid);
-                above = first ? before : before + h0;
+            uint32_t before = block_scan(h.x + h.y + h.z + h.w, wsum, total);
+            const uint32_t down[4] = {h.w, h.z, h.y, h.x};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (before < left && left <= before + down[i]) {
+                    pick = (uint32_t)(BINS - 1 - 4 * tid - i);
+                    above = before;
+                }
+                before += down[i];
             }
             __syncthreads();
             prefix |= pick << shift;
-            mask |= ((1u << bits) - 1u) << shift;
+            mask |= digit << shift;
             left -= above;
             __syncthreads();
         }
         ties = left;                                   // this many of the tokens whose key is `prefix`, in order
     }
-    // ---- kept positions in order ----
-    uint32_t done = 0, tied = 0;                       // kept so far; of them equal to the last kept key
-    if (need > 0) {
-        const bool all = need == C;
-        for (int base = 0; base < C; base += SEL_THREADS) {
-            const int t = base + tid;
-            const float x = t < C ? w[t] : 0.f;
-            const uint32_t k = order_key(x);
-            const bool gt = t < C && (all || k > prefix), eq = t < C && !all && k == prefix;
-            // two counts in one sum: larger keys low, equal keys high (at most 1024 each)
+    // larger keys (low half: at most 8 per thread of 512) and equal ones (high half) of a thread's tokens
+    auto count = [&](int base) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < SEL_ITEMS; ++i) {
+            const uint32_t k = order_key(x[i]);
+            if (base + SEL_ITEMS * tid + i < end) c += all || k > prefix ? 1u : (k == prefix ? 1u << 16 : 0u);
+        }
+        return c;
+    };
+    uint32_t larger = 0, tied = 0;                     // before this CTA's tokens, then before the tile's
+    if (cluster_size > 1) {
+        uint32_t g = 0, e = 0;
+        for (int base = begin; base < end; base += SEL_TILE) {
+            if (!once) load(base);
             uint32_t total;
-            const uint32_t sc = block_scan((gt ? 1u : 0u) | (eq ? 1u << 16 : 0u), wsum, total);
-            const uint32_t eq_before = tied + (sc >> 16);
-            const bool keep = gt || (eq && eq_before < ties);
-            if (keep) {
-                const uint32_t at = done + (sc & 0xffffu) + min(eq_before, ties) - min(tied, ties);
-                kept[at] = t;
-                if (nw) nw[at] = x;
-            }
-            const uint32_t eq_now = min(tied + (total >> 16), ties) - min(tied, ties);
-            done += (total & 0xffffu) + eq_now;
-            tied += total >> 16;
+            block_scan(count(base), wsum, total);
+            g += total & 0xffffu;
+            e += total >> 16;
+        }
+        if (tid == 0) {
+            mine[0] = g;
+            mine[1] = e;
+        }
+        cluster.sync();
+        for (int q = 0; q < rank; ++q) {
+            const uint32_t *theirs = cluster.map_shared_rank(&mine[0], q);
+            larger += theirs[0];
+            tied += theirs[1];
         }
     }
-    for (int i = tid; i < tail; i += SEL_THREADS) {
-        kept[need + i] = C + i;
-        if (nw) nw[need + i] = w[C + i];
+    // ---- kept positions in order ----
+    for (int base = begin; base < end; base += SEL_TILE) {
+        if (!once) load(base);
+        uint32_t total;
+        const uint32_t sc = block_scan(count(base), wsum, total);
+        uint32_t g = larger + (sc & 0xffffu), e = tied + (sc >> 16);
+#pragma unroll
+        for (int i = 0; i < SEL_ITEMS; ++i) {
+            const int t = base + SEL_ITEMS * tid + i;
+            const uint32_t k = order_key(x[i]);
+            if (t >= end) break;
+            const bool gt = all || k > prefix, eq = !all && k == prefix;
+            if (gt || (eq && e < ties)) {
+                const uint32_t at = g + min(e, ties);
+                kept[at] = t;
+                if (nw) nw[at] = x[i];
+            }
+            g += gt;
+            e += eq;
+        }
+        larger += total & 0xffffu;
+        tied += total >> 16;
     }
+    cluster.sync();                                    // no CTA leaves while its counts are read
 }
 
 template <int D, bool Q8>
@@ -136,6 +212,7 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) k_evict_move(KvEvictArgs A, l
     constexpr int RPI = 32 / CH;             // rows per warp access
     constexpr int LOADS = KV_BLOCK / RPI;
     const int lane = threadIdx.x % 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long u = (long)blockIdx.x * MOVE_WARPS + threadIdx.x / 32;
     if (u >= units) return;
     const bool is_v = u & 1;
@@ -198,18 +275,45 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) k_evict_move(KvEvictArgs A, l
     }
 }
 
+// The select, or with `dependent` the move as its programmatic dependent.
+template <typename... P, typename... V>
+cudaError_t launch_ex(void (*k)(P...), unsigned grid, unsigned threads, int cluster, bool dependent, cudaStream_t s,
+                      V... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    if (dependent) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+    } else {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
 template <int D, bool Q8> cudaError_t launch_move(const KvEvictArgs &A, int *err, cudaStream_t s) {
     const int nblocks = (A.budget + KV_BLOCK - 1) / KV_BLOCK;
     const long units = (long)A.B * A.pg.Hkv * nblocks * 2;
-    k_evict_move<D, Q8><<<(unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_WARPS * 32, 0, s>>>(A, units, nblocks, err);
-    return cudaGetLastError();
+    return launch_ex(k_evict_move<D, Q8>, (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_WARPS * 32, 1, true, s,
+                     A, units, nblocks, err);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_evict(const KvEvictArgs &A, const DeviceCtl &ctl, cudaStream_t s) {
-    k_evict_select<<<(unsigned)((long)A.B * A.pg.Hkv), SEL_THREADS, 0, s>>>(A);
-    cudaError_t e = cudaGetLastError();
+cudaError_t launch_kv_evict(const KvEvictArgs &A, int sm_count, const DeviceCtl &ctl, cudaStream_t s) {
+    // up to 8 CTAs per head (the portable cluster size) while a CTA's share is more than
+    // it keeps in registers and the heads alone do not fill the machine
+    const long heads = (long)A.B * A.pg.Hkv;
+    const int cap = A.pg.max_pages << A.pg.pshift;
+    int cl = 1;
+    while (cl < 8 && cap > cl * SEL_TILE && heads * cl < 2 * sm_count) cl *= 2;
+    cudaError_t e = launch_ex(k_evict_select, (unsigned)(heads * cl), SEL_THREADS, cl, false, s, A, cl);
     if (e != cudaSuccess) return e;
     if (A.d == 64) return A.kexp ? launch_move<64, true>(A, ctl.err, s) : launch_move<64, false>(A, ctl.err, s);
     return A.kexp ? launch_move<128, true>(A, ctl.err, s) : launch_move<128, false>(A, ctl.err, s);
