@@ -11,7 +11,7 @@
 // bits) and writes the kept positions in order: a cluster of CTAs per head, whose
 // histograms meet in distributed shared memory; a CTA whose share is at most
 // SEL_TILE tokens reads its weights once and keeps the keys in registers.
-// k_evict_move copies the rows, one warp per 16-row destination block.  An e4m3
+// k_evict_move copies the rows, one warp per 16-row destination block (K and V).  An e4m3
 // destination block takes the largest exponent of its rows' source blocks and the
 // rows of smaller ones are moved to it (exact until subnormal).
 #include <cooperative_groups.h>
@@ -28,7 +28,8 @@ constexpr int SEL_TILE = SEL_THREADS * SEL_ITEMS;
 constexpr int BINS = 2048;
 constexpr int MOVE_WARPS = 4;
 
-// Weights as integers in the same order: -0 and +0 are equal, NaN is -inf.
+// Weights as integers in the same order: -0 and +0 are equal, NaN is -inf.  The
+// smallest key is 0x007fffff; 0 stands for no token.
 __device__ __forceinline__ uint32_t order_key(float x) {
     uint32_t u = __float_as_uint(x);
     if ((u & 0x7fffffffu) > 0x7f800000u) u = 0xff800000u;
@@ -59,9 +60,17 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *wsum, uint3
     return x - v + (warp > 0 ? before : 0u);
 }
 
-__global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A, int cluster_size) {
+template <bool CLUSTER>
+__global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(KvEvictArgs A, int ctas) {
     namespace cg = cooperative_groups;
     const cg::cluster_group cluster = cg::this_cluster();
+    const int cluster_size = CLUSTER ? ctas : 1;
+    auto sync = [&] {
+        if constexpr (CLUSTER)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
     __shared__ __align__(16) uint32_t hist[3][BINS];
     __shared__ uint32_t wsum[32];
     __shared__ uint32_t pick, above, mine[2];
@@ -88,16 +97,16 @@ __global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A, int
     const int begin = min(rank * share, C), end = min(begin + share, C);
     const bool all = need == C, once = share <= SEL_TILE;
 
-    float x[SEL_ITEMS];
-    auto load = [&](int base) {                        // tokens base + 8 tid ..; past `end`: not looked at
+    uint32_t key[SEL_ITEMS];
+    auto load = [&](int base) {                        // tokens base + 8 tid ..
 #pragma unroll
         for (int v = 0; v < SEL_ITEMS; v += 4) {
             const int t = base + SEL_ITEMS * tid + v;
             const float4 f = t < end ? *reinterpret_cast<const float4 *>(w + t) : make_float4(0.f, 0.f, 0.f, 0.f);
-            x[v] = f.x;
-            x[v + 1] = f.y;
-            x[v + 2] = f.z;
-            x[v + 3] = f.w;
+            key[v] = t < end ? order_key(f.x) : 0u;
+            key[v + 1] = t + 1 < end ? order_key(f.y) : 0u;
+            key[v + 2] = t + 2 < end ? order_key(f.z) : 0u;
+            key[v + 3] = t + 3 < end ? order_key(f.w) : 0u;
         }
     };
     if (once) load(begin);
@@ -113,16 +122,17 @@ __global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A, int
                 if (!once) load(base);
 #pragma unroll
                 for (int i = 0; i < SEL_ITEMS; ++i) {
-                    const uint32_t k = order_key(x[i]);
-                    if (base + SEL_ITEMS * tid + i < end && (k & mask) == prefix)
-                        atomicAdd(&hist[pass][(k >> shift) & digit], 1u);
+                    const uint32_t k = key[i];
+                    if ((k & mask) == prefix && k != 0u) atomicAdd(&hist[pass][(k >> shift) & digit], 1u);
                 }
             }
-            cluster.sync();                            // every CTA's histogram of this digit is complete
+            sync();                                    // every CTA's histogram of this digit is complete
             // thread i owns bins 2047 - 4 i .. 2044 - 4 i: an exclusive sum from the largest bin down
             uint4 h = make_uint4(0u, 0u, 0u, 0u);
-            for (int q = 0; q < cluster_size; ++q) {
-                const uint32_t *theirs = cluster.map_shared_rank(&hist[pass][0], q);
+#pragma unroll
+            for (int q = 0; q < (CLUSTER ? 8 : 1); ++q) {
+                if (q >= cluster_size) break;
+                const uint32_t *theirs = CLUSTER ? cluster.map_shared_rank(&hist[pass][0], q) : &hist[pass][0];
                 const uint4 o = *reinterpret_cast<const uint4 *>(theirs + BINS - 4 - 4 * tid);
                 h.x += o.x;
                 h.y += o.y;
@@ -144,27 +154,24 @@ __global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A, int
             prefix |= pick << shift;
             mask |= digit << shift;
             left -= above;
-            __syncthreads();
         }
         ties = left;                                   // this many of the tokens whose key is `prefix`, in order
     }
-    // larger keys (low half: at most 8 per thread of 512) and equal ones (high half) of a thread's tokens
-    auto count = [&](int base) {
+    // Larger keys (low half: at most 8 per thread of 512) and equal ones (high half) of a
+    // thread's tokens; when all are kept, prefix and ties are 0.
+    auto count = [&] {
         uint32_t c = 0;
 #pragma unroll
-        for (int i = 0; i < SEL_ITEMS; ++i) {
-            const uint32_t k = order_key(x[i]);
-            if (base + SEL_ITEMS * tid + i < end) c += all || k > prefix ? 1u : (k == prefix ? 1u << 16 : 0u);
-        }
+        for (int i = 0; i < SEL_ITEMS; ++i) c += key[i] > prefix ? 1u : (key[i] == prefix ? 1u << 16 : 0u);
         return c;
     };
     uint32_t larger = 0, tied = 0;                     // before this CTA's tokens, then before the tile's
-    if (cluster_size > 1) {
+    if constexpr (CLUSTER) {
         uint32_t g = 0, e = 0;
         for (int base = begin; base < end; base += SEL_TILE) {
             if (!once) load(base);
             uint32_t total;
-            block_scan(count(base), wsum, total);
+            block_scan(count(), wsum, total);
             g += total & 0xffffu;
             e += total >> 16;
         }
@@ -183,18 +190,16 @@ __global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A, int
     for (int base = begin; base < end; base += SEL_TILE) {
         if (!once) load(base);
         uint32_t total;
-        const uint32_t sc = block_scan(count(base), wsum, total);
+        const uint32_t sc = block_scan(count(), wsum, total);
         uint32_t g = larger + (sc & 0xffffu), e = tied + (sc >> 16);
 #pragma unroll
         for (int i = 0; i < SEL_ITEMS; ++i) {
-            const int t = base + SEL_ITEMS * tid + i;
-            const uint32_t k = order_key(x[i]);
-            if (t >= end) break;
-            const bool gt = all || k > prefix, eq = !all && k == prefix;
+            const bool gt = key[i] > prefix, eq = key[i] == prefix;
             if (gt || (eq && e < ties)) {
+                const int t = base + SEL_ITEMS * tid + i;
                 const uint32_t at = g + min(e, ties);
                 kept[at] = t;
-                if (nw) nw[at] = x[i];
+                if (nw) nw[at] = w[t];
             }
             g += gt;
             e += eq;
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(SEL_THREADS) k_evict_select(KvEvictArgs A, int
         larger += total & 0xffffu;
         tied += total >> 16;
     }
-    cluster.sync();                                    // no CTA leaves while its counts are read
+    if constexpr (CLUSTER) cluster.sync();             // no CTA leaves while its counts are read
 }
 
 template <int D, bool Q8>
@@ -215,9 +220,8 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) k_evict_move(KvEvictArgs A, l
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long u = (long)blockIdx.x * MOVE_WARPS + threadIdx.x / 32;
     if (u >= units) return;
-    const bool is_v = u & 1;
-    const int blk = (int)((u >> 1) % nblocks);
-    const long bk = (u >> 1) / nblocks;
+    const int blk = (int)(u % nblocks);
+    const long bk = u / nblocks;
     const int b = (int)(bk / A.pg.Hkv), kvh = (int)(bk % A.pg.Hkv);
     const int ps = 1 << A.pg.pshift;
     const int L = min(max(A.seqlens[b], 0), A.pg.max_pages << A.pg.pshift);
@@ -230,48 +234,57 @@ __global__ void __launch_bounds__(MOVE_WARPS * 32) k_evict_move(KvEvictArgs A, l
         if (lane == 0) atomicExch(err, PARALLAX_ERR_DEVICE_INDEX);
         return;
     }
-    uint8_t *pages = static_cast<uint8_t *>(is_v ? A.vpages : A.kpages);
-    signed char *exps = is_v ? A.vexp : A.kexp;
     // lane i < rows: where row i comes from (-1: a page id out of range, the row is zero)
     long long from = -1;
-    int e = KV_EMIN;
+    int e[2] = {KV_EMIN, KV_EMIN};
     if (lane < rows) {
         const int t = A.kept[(size_t)bk * A.budget + i0 + lane];
         const int id = A.pg.table[(size_t)b * A.pg.max_pages + (t >> A.pg.pshift)];
         if ((unsigned)id < (unsigned)A.pg.num_pages) {
             const size_t slab = (size_t)id * A.pg.Hkv + kvh;
             from = (long long)(slab * ps + (t & (ps - 1)));
-            if constexpr (Q8) e = exps[slab * (ps / KV_BLOCK) + (t & (ps - 1)) / KV_BLOCK];
+            if constexpr (Q8) {
+                e[0] = A.kexp[slab * (ps / KV_BLOCK) + (t & (ps - 1)) / KV_BLOCK];
+                e[1] = A.vexp[slab * (ps / KV_BLOCK) + (t & (ps - 1)) / KV_BLOCK];
+            }
         } else {
             atomicExch(err, PARALLAX_ERR_DEVICE_INDEX);
         }
     }
     const size_t dslab = (size_t)did * A.pg.Hkv + kvh;
     const int drow = i0 & (ps - 1);
-    uint8_t *dst = pages + (dslab * ps + drow) * ROW;
     const int ch = lane % CH, rr = lane / CH;
-    uint4 w[LOADS];
+    uint8_t *const pages[2] = {static_cast<uint8_t *>(A.kpages), static_cast<uint8_t *>(A.vpages)};
+    uint4 w[2][LOADS];                                         // K and V rows: all loads before the first store
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        const int row = i * RPI + rr;
-        const long long f = __shfl_sync(0xffffffffu, from, row);
-        w[i] = f >= 0 ? *reinterpret_cast<const uint4 *>(pages + f * ROW + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if constexpr (Q8) {
-        int emax = e;
+        const long long f = __shfl_sync(0xffffffffu, from, i * RPI + rr);
 #pragma unroll
-        for (int off = 16; off > 0; off /= 2) emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, off));
+        for (int x = 0; x < 2; ++x)
+            w[x][i] = f >= 0 ? *reinterpret_cast<const uint4 *>(pages[x] + f * ROW + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        if constexpr (Q8) {
+            int emax = e[x];
+#pragma unroll
+            for (int off = 16; off > 0; off /= 2) emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, off));
+            // in most blocks all rows share an exponent or most do; a row below it is moved to it
+            if (__any_sync(0xffffffffu, lane < rows && e[x] != emax)) {
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) {
+                    const int es = __shfl_sync(0xffffffffu, e[x], i * RPI + rr);
+                    if (es < emax) w[x][i] = e4m3_shift_down(w[x][i], emax - es);
+                }
+            }
+            if (lane == 0) (x ? A.vexp : A.kexp)[dslab * (ps / KV_BLOCK) + drow / KV_BLOCK] = (signed char)emax;
+        }
+        uint8_t *dst = pages[x] + (dslab * ps + drow) * ROW;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int es = __shfl_sync(0xffffffffu, e, i * RPI + rr);
-            if (es < emax) w[i] = e4m3_shift_down(w[i], emax - es);
+            const int row = i * RPI + rr;
+            if (row < rows) *reinterpret_cast<uint4 *>(dst + row * ROW + ch * 16) = w[x][i];
         }
-        if (lane == 0) exps[dslab * (ps / KV_BLOCK) + drow / KV_BLOCK] = (signed char)emax;
-    }
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        const int row = i * RPI + rr;
-        if (row < rows) *reinterpret_cast<uint4 *>(dst + row * ROW + ch * 16) = w[i];
     }
 }
 
@@ -299,7 +312,7 @@ cudaError_t launch_ex(void (*k)(P...), unsigned grid, unsigned threads, int clus
 
 template <int D, bool Q8> cudaError_t launch_move(const KvEvictArgs &A, int *err, cudaStream_t s) {
     const int nblocks = (A.budget + KV_BLOCK - 1) / KV_BLOCK;
-    const long units = (long)A.B * A.pg.Hkv * nblocks * 2;
+    const long units = (long)A.B * A.pg.Hkv * nblocks;
     return launch_ex(k_evict_move<D, Q8>, (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_WARPS * 32, 1, true, s,
                      A, units, nblocks, err);
 }
@@ -313,7 +326,8 @@ cudaError_t launch_kv_evict(const KvEvictArgs &A, int sm_count, const DeviceCtl 
     const int cap = A.pg.max_pages << A.pg.pshift;
     int cl = 1;
     while (cl < 8 && cap > cl * SEL_TILE && heads * cl < 2 * sm_count) cl *= 2;
-    cudaError_t e = launch_ex(k_evict_select, (unsigned)(heads * cl), SEL_THREADS, cl, false, s, A, cl);
+    cudaError_t e = cl > 1 ? launch_ex(k_evict_select<true>, (unsigned)(heads * cl), SEL_THREADS, cl, false, s, A, cl)
+                           : launch_ex(k_evict_select<false>, (unsigned)heads, SEL_THREADS, 1, false, s, A, 1);
     if (e != cudaSuccess) return e;
     if (A.d == 64) return A.kexp ? launch_move<64, true>(A, ctl.err, s) : launch_move<64, false>(A, ctl.err, s);
     return A.kexp ? launch_move<128, true>(A, ctl.err, s) : launch_move<128, false>(A, ctl.err, s);
