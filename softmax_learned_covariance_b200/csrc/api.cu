@@ -543,7 +543,8 @@ int parallax_kv_append(const void *k, const void *v, const long long *k_strides,
     KvAppendArgs A{k, v, {}, {}, kpages, vpages, kexp, vexp, {}, seqlens, counts, new_seqlens, wacc, B, T, d};
     int st = paged_layout(block_table, B, Hkv, page_size, max_pages, num_pages, d, &A.pg);
     if (st) return st;
-    if (T < 1 || T > (1 << 30) || (__int128)B * Hkv * T > ((__int128)1 << 34)) return PARALLAX_ERR_SHAPE;
+    // a warp per block of 16 tokens, head and K or V, one grid
+    if (T < 1 || T > (1 << 30) || (__int128)B * Hkv * ((T + 30) / 16) * 2 >= ((__int128)1 << 31)) return PARALLAX_ERR_SHAPE;
     if (in_dtype != PARALLAX_BF16) return PARALLAX_ERR_DTYPE;
     if ((st = cache_dtype_ok(cache_dtype, kexp, vexp))) return st;
     for (int i = 0; i < 3; ++i) {
@@ -576,7 +577,7 @@ int parallax_kv_evict(void *kpages, void *vpages, signed char *kexp, signed char
     if (st) return st;
     if ((st = paged_layout(block_table, B, Hkv, page_size, max_pages, num_pages, d, &A.pg))) return st;
     if (budget < 1 || recent < 0 || recent > budget || budget > (long long)new_max_pages * page_size ||
-        (long long)B * Hkv > (1ll << 28) || (__int128)B * Hkv * budget > ((__int128)1 << 34))
+        (long long)B * Hkv > (1ll << 28) || (__int128)B * Hkv * ((budget + 15) / 16) >= ((__int128)1 << 31))
         return PARALLAX_ERR_SHAPE;
     if ((st = cache_dtype_ok(cache_dtype, kexp, vexp))) return st;
     if (!aligned16(kpages) || !aligned16(vpages) || !aligned4(block_table) || !aligned4(seqlens) || !aligned16(wacc) ||

@@ -47,17 +47,17 @@ __device__ __forceinline__ uint32_t cvt4(uint32_t a, uint32_t b, float f) {
 }
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(WARPS * 32) k_kv_append(KvAppendArgs A, long units, int nblocks, int *__restrict__ err) {
+__global__ void __launch_bounds__(WARPS * 32) k_kv_append(KvAppendArgs A, unsigned units, unsigned nblocks, int *__restrict__ err) {
     constexpr int CH = D / 8;             // 16-byte chunks of a bf16 row
     constexpr int RPI = 32 / CH;          // rows per warp load
     constexpr int LOADS = KV_BLOCK / RPI;
     const int lane = threadIdx.x % 32;
-    const long u = (long)blockIdx.x * WARPS + threadIdx.x / 32;
+    const unsigned u = blockIdx.x * WARPS + threadIdx.x / 32;
     if (u >= units) return;
     const bool is_v = u & 1;
     const int blk = (int)((u >> 1) % nblocks);
-    const long bk = (u >> 1) / nblocks;
-    const int b = (int)(bk / A.pg.Hkv), kvh = (int)(bk % A.pg.Hkv);
+    const unsigned bk = (u >> 1) / nblocks;
+    const int b = (int)(bk / (unsigned)A.pg.Hkv), kvh = (int)(bk % (unsigned)A.pg.Hkv);
     const int ps = 1 << A.pg.pshift, cap = A.pg.max_pages << A.pg.pshift;
     const int start = min(max(A.seqlens[b], 0), cap);
     int n = A.counts ? min(max(A.counts[b], 0), A.T) : A.T;
@@ -142,9 +142,9 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_append(KvAppendArgs A, long u
 }
 
 template <int D, bool Q8> cudaError_t launch_t(const KvAppendArgs &A, int *err, cudaStream_t s) {
-    const int nblocks = (A.T + KV_BLOCK - 1 + KV_BLOCK - 1) / KV_BLOCK;    // blocks T tokens can touch
-    const long units = (long)A.B * A.pg.Hkv * nblocks * 2;
-    k_kv_append<D, Q8><<<(unsigned)((units + WARPS - 1) / WARPS), WARPS * 32, 0, s>>>(A, units, nblocks, err);
+    const unsigned nblocks = (unsigned)(A.T + KV_BLOCK - 1 + KV_BLOCK - 1) / KV_BLOCK;    // blocks T tokens can touch
+    const unsigned units = (unsigned)A.B * A.pg.Hkv * nblocks * 2;                        // below 2^31 (checked at entry)
+    k_kv_append<D, Q8><<<(units + WARPS - 1) / WARPS, WARPS * 32, 0, s>>>(A, units, nblocks, err);
     return cudaGetLastError();
 }
 

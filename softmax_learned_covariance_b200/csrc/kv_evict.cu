@@ -75,15 +75,15 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
     __shared__ uint32_t wsum[32];
     __shared__ uint32_t pick, above, mine[2];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, rank = blockIdx.x % cluster_size;
-    const long bk = blockIdx.x / cluster_size;
-    const int b = (int)(bk / A.pg.Hkv);
+    const int tid = threadIdx.x, rank = CLUSTER ? (int)(blockIdx.x % (unsigned)cluster_size) : 0;
+    const unsigned bk = blockIdx.x / (unsigned)cluster_size;
+    const int b = (int)(bk / (unsigned)A.pg.Hkv);
     const int cap = A.pg.max_pages << A.pg.pshift;
     const size_t ncap = (size_t)A.new_max_pages << A.pg.pshift;
     const int L = min(max(A.seqlens[b], 0), cap);
     const int n = min(L, A.budget), tail = min(A.recent, n);
     const int C = L - tail, need = n - tail;           // `need` of the first C, then the last `tail`
-    if (bk % A.pg.Hkv == 0 && rank == 0 && tid == 0) A.new_seqlens[b] = n;
+    if (bk == (unsigned)b * A.pg.Hkv && rank == 0 && tid == 0) A.new_seqlens[b] = n;
     const float *w = A.wacc + (size_t)bk * cap;
     int *kept = A.kept + (size_t)bk * A.budget;
     float *nw = A.new_wacc ? A.new_wacc + bk * ncap : nullptr;
@@ -211,18 +211,18 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
 }
 
 template <int D, bool Q8>
-__global__ void __launch_bounds__(MOVE_WARPS * 32) k_evict_move(KvEvictArgs A, long units, int nblocks, int *__restrict__ err) {
+__global__ void __launch_bounds__(MOVE_WARPS * 32) k_evict_move(KvEvictArgs A, unsigned units, unsigned nblocks, int *__restrict__ err) {
     constexpr int ROW = D * (Q8 ? 1 : 2);
     constexpr int CH = ROW / 16;             // 16-byte chunks of a row
     constexpr int RPI = 32 / CH;             // rows per warp access
     constexpr int LOADS = KV_BLOCK / RPI;
     const int lane = threadIdx.x % 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long u = (long)blockIdx.x * MOVE_WARPS + threadIdx.x / 32;
+    const unsigned u = blockIdx.x * MOVE_WARPS + threadIdx.x / 32;
     if (u >= units) return;
     const int blk = (int)(u % nblocks);
-    const long bk = u / nblocks;
-    const int b = (int)(bk / A.pg.Hkv), kvh = (int)(bk % A.pg.Hkv);
+    const unsigned bk = u / nblocks;
+    const int b = (int)(bk / (unsigned)A.pg.Hkv), kvh = (int)(bk % (unsigned)A.pg.Hkv);
     const int ps = 1 << A.pg.pshift;
     const int L = min(max(A.seqlens[b], 0), A.pg.max_pages << A.pg.pshift);
     const int n = min(L, A.budget);
@@ -311,9 +311,9 @@ cudaError_t launch_ex(void (*k)(P...), unsigned grid, unsigned threads, int clus
 }
 
 template <int D, bool Q8> cudaError_t launch_move(const KvEvictArgs &A, int *err, cudaStream_t s) {
-    const int nblocks = (A.budget + KV_BLOCK - 1) / KV_BLOCK;
-    const long units = (long)A.B * A.pg.Hkv * nblocks;
-    return launch_ex(k_evict_move<D, Q8>, (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_WARPS * 32, 1, true, s,
+    const unsigned nblocks = (unsigned)(A.budget + KV_BLOCK - 1) / KV_BLOCK;
+    const unsigned units = (unsigned)A.B * A.pg.Hkv * nblocks;      // below 2^31 (checked at entry)
+    return launch_ex(k_evict_move<D, Q8>, (units + MOVE_WARPS - 1) / MOVE_WARPS, MOVE_WARPS * 32, 1, true, s,
                      A, units, nblocks, err);
 }
 
