@@ -5,7 +5,8 @@ key/value covariance projected by a learned probe rho_i = W_R x_i (zubnet.ai
 news item on Parallax, paragraph 2):  y_i = o_i - (m_i - o_i abar_i).
 
 This module only marshals torch tensors to the shared library
-``libparallax.so`` (built by ``softmax_learned_covariance_b200.build``); every
+``libparallax.so`` (built by ``softmax_learned_covariance_b200.build``, as is the
+native part of the marshalling, ``_binding.so``); every
 step of the computation runs in its CUDA kernels.  There is no fallback: if the
 library is missing or a call fails, a ``ParallaxError`` is raised.
 
@@ -312,62 +313,36 @@ def parallax_decode_paged(q, rho, kpages, vpages, block_table, seqlens, out_dtyp
     return y, lse
 
 
-def _is(t, name, dtype, shape, device):
-    """A tensor a kernel reads or writes whole: contiguous, on `device`, of this dtype and shape."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+_bound = None
 
 
-def _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens):
-    """Shapes of a paged cache; returns (device, B, Hkv, page_size, max_pages, num_pages, d, dtype code)."""
-    _need(kpages, "kpages")
-    if kpages.dim() != 4 or block_table.dim() != 2 or kpages.shape[2] < 16:
-        raise ValueError("kpages must be [num_pages, Hkv, page_size >= 16, d] and block_table [B, max_pages]")
-    dev, dtype = kpages.device, kpages.dtype
-    num_pages, Hkv, page_size, d = kpages.shape
-    B, max_pages = block_table.shape
-    _is(vpages, "vpages", dtype, kpages.shape, dev)
-    if dtype == torch.float8_e4m3fn:
-        if kexp is None or vexp is None:
-            raise ValueError("an e4m3 cache needs kexp and vexp")
-        _is(kexp, "kexp", torch.int8, (num_pages, Hkv, page_size // 16), dev)
-        _is(vexp, "vexp", torch.int8, (num_pages, Hkv, page_size // 16), dev)
-        code = E4M3
-    elif dtype == torch.bfloat16:
-        if kexp is not None or vexp is not None:
-            raise ValueError("a bf16 cache has no exponents")
-        code = BF16
-    else:
-        raise TypeError(f"unsupported cache dtype {dtype}")
-    _is(block_table, "block_table", torch.int32, (B, max_pages), dev)
-    _is(seqlens, "seqlens", torch.int32, (B,), dev)
-    return dev, B, Hkv, page_size, max_pages, num_pages, d, code
-
-
-def _elsewhere(torch, device, stream):
-    """Whether a call has to change the current device or stream first (see _on)."""
-    return stream is not None or device.index != torch.cuda.current_device()
+def _native():
+    """The native part of the binding (csrc/binding.cpp) with the loaded library's entry points."""
+    global _bound
+    L = lib()
+    if _bound is not L:
+        _torch()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ParallaxError(-1, f"the native binding does not load ({e}); build it with "
+                                    "`python -m softmax_learned_covariance_b200.build`") from e
+        _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                        (L.parallax_decode_paged_q8, L.parallax_decode_paged_acc, L.parallax_kv_append,
+                         L.parallax_kv_evict)))
+        _native.module = _binding
+        _bound = L
+    return _native.module
 
 
 @contextlib.contextmanager
-def _on(torch, device, stream):
-    """The tensors' device as the current one and `stream` (default: its current one) as its current
-    stream, so that outputs allocated inside belong to the stream that writes them."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream must be one of {device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+def _on(pages, stream):
+    """`stream` as the current stream of the tensors' device, so that outputs allocated inside belong to
+    the stream that writes them."""
+    if stream.device != pages.device:
+        raise ValueError(f"the stream must be one of {pages.device}")
+    with _torch().cuda.stream(stream):
         yield
-
-
-def _raw_stream(torch, device):
-    # the handle of torch.cuda.current_stream(device) without building a Stream (0.1 against 2.2 us a call)
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
 
 
 def parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp=None, vexp=None, counts=None,
@@ -379,75 +354,13 @@ def parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp=None, ve
     vexp int8 [num_pages, Hkv, page_size / 16].  counts: int32 [B], tokens of each sequence (default
     T).  wacc: the weight accumulator, whose entries of the new tokens become 0.
     """
-    torch = _torch()
-    dev, B, Hkv, ps, mp, npg, d, code = _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens)
-    T = k.shape[2] if k.dim() == 4 else 0
-    strides = []
-    for t, n in ((k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{n} must be bfloat16")
-        if t.shape != (B, Hkv, T, d) or t.device != dev:
-            raise ValueError(f"{n} must be [B, Hkv, T, d] = [{B}, {Hkv}, T, {d}] on {dev}")
-        if t.is_contiguous():
-            strides.append(None)
-            continue
-        sb, sh, st, si = t.stride()
-        if si != 1:
-            raise ValueError(f"{n} must have a dense last dimension")
-        # the stride of a dimension of size 1 means nothing
-        strides.append((ctypes.c_longlong * 3)(sb if B > 1 else 0, sh if Hkv > 1 else 0, st if T > 1 else 0))
-    if counts is not None:
-        _is(counts, "counts", torch.int32, (B,), dev)
-    if wacc is not None:
-        _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
-    if _elsewhere(torch, dev, stream):
-        with _on(torch, dev, stream):
+    if stream is not None:
+        with _on(kpages, stream):
             return parallax_kv_append(k, v, kpages, vpages, block_table, seqlens, kexp, vexp, counts, new_seqlens, wacc)
-    if new_seqlens is None:
-        new_seqlens = torch.empty_like(seqlens)
-    else:
-        _is(new_seqlens, "new_seqlens", torch.int32, (B,), dev)
-    st = lib().parallax_kv_append(_at(k), _at(v), strides[0], strides[1], _at(kpages), _at(vpages), _at(kexp),
-                                  _at(vexp), _at(block_table), _at(seqlens), _at(counts), _at(new_seqlens), _at(wacc),
-                                  B, Hkv, T, ps, mp, npg, d, BF16, code, _raw_stream(torch, dev))
-    _check(st, "parallax_kv_append")
-    return new_seqlens
-
-
-def _decode_cache(name, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, out_dtype, y, lse, stream,
-                  want_lse):
-    torch = _torch()
-    dev, B, Hkv, ps, mp, npg, d, code = _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [B, Hq, d] = [{B}, Hq, {d}]")
-    Hq = q.shape[1]
-    _is(q, "q", torch.bfloat16, (B, Hq, d), dev)
-    if rho is not None:
-        _is(rho, "rho", torch.bfloat16, (B, Hq, d), dev)
-    if wacc is not None:
-        _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
-    if _elsewhere(torch, dev, stream):
-        with _on(torch, dev, stream):
-            return _decode_cache(name, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, out_dtype, y,
-                                 lse, None, want_lse)
-    if y is None:
-        y = torch.empty_like(q, dtype=out_dtype or torch.float32)
-    else:
-        _is(y, "y", y.dtype, (B, Hq, d), dev)
-    if lse is not None:
-        _is(lse, "lse", torch.float32, (B, Hq), dev)
-    elif want_lse:
-        lse = q.new_empty((B, Hq), dtype=torch.float32)
-    if code == E4M3:
-        st = lib().parallax_decode_paged_q8(_at(q), _at(rho), _at(kpages), _at(vpages), _at(kexp), _at(vexp),
-                                            _at(block_table), _at(seqlens), _at(y), _at(lse), _at(wacc), B, Hq, Hkv,
-                                            ps, mp, npg, d, BF16, _dtype_code(y.dtype), _raw_stream(torch, dev))
-    else:
-        st = lib().parallax_decode_paged_acc(_at(q), _at(rho), _at(kpages), _at(vpages), _at(block_table),
-                                             _at(seqlens), _at(y), _at(lse), _at(wacc), B, Hq, Hkv, ps, mp, npg, d,
-                                             BF16, _dtype_code(y.dtype), _raw_stream(torch, dev))
-    _check(st, name)
-    return y, lse
+    r = _native().append(k, v, kpages, vpages, kexp, vexp, block_table, seqlens, counts, new_seqlens, wacc)
+    if type(r) is int:
+        _check(r, "parallax_kv_append")
+    return r
 
 
 def parallax_decode_paged_q8(q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc=None, out_dtype=None,
@@ -459,21 +372,39 @@ def parallax_decode_paged_q8(q, rho, kpages, vpages, kexp, vexp, block_table, se
     [B, Hkv, max_pages * page_size], to which the attention weight of each cached token, summed over
     the query heads of its KV head, is added.
     """
-    if kpages.dtype != _torch().float8_e4m3fn:
+    torch = _torch()
+    if kpages.dtype != torch.float8_e4m3fn:
         raise TypeError("kpages must be float8_e4m3fn")
-    return _decode_cache("parallax_decode_paged_q8", q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc,
-                         out_dtype, y, lse, stream, want_lse)
+    return _decode_cache("parallax_decode_paged_q8", torch, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens,
+                         wacc, out_dtype, y, lse, stream, want_lse)
 
 
 def parallax_decode_paged_acc(q, rho, kpages, vpages, block_table, seqlens, wacc, out_dtype=None, y=None, lse=None,
                               stream=None, want_lse: bool = True):
     """parallax_decode_paged_q8 over a bf16 paged cache; wacc is required."""
-    if kpages.dtype != _torch().bfloat16:
+    torch = _torch()
+    if kpages.dtype != torch.bfloat16:
         raise TypeError("kpages must be bfloat16")
     if wacc is None:
         raise ValueError("wacc is required; without it use parallax_decode_paged")
-    return _decode_cache("parallax_decode_paged_acc", q, rho, kpages, vpages, None, None, block_table, seqlens, wacc,
-                         out_dtype, y, lse, stream, want_lse)
+    return _decode_cache("parallax_decode_paged_acc", torch, q, rho, kpages, vpages, None, None, block_table, seqlens,
+                         wacc, out_dtype, y, lse, stream, want_lse)
+
+
+def _decode_cache(name, torch, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, out_dtype, y, lse,
+                  stream, want_lse):
+    if out_dtype is not None and out_dtype != torch.float32 and out_dtype != torch.bfloat16:
+        raise TypeError(f"unsupported dtype {out_dtype}")
+    args = (q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, y, lse, out_dtype == torch.bfloat16,
+            bool(want_lse))
+    if stream is None:
+        r = _native().decode(*args)
+    else:
+        with _on(kpages, stream):
+            r = _native().decode(*args)
+    if type(r) is int:
+        _check(r, name)
+    return r
 
 
 def parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, budget: int, recent: int, kexp=None,
@@ -485,37 +416,16 @@ def parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, bud
     new_wacc fp32 [B, Hkv, new_max_pages * page_size]); kept and new_wacc are written up to each
     sequence's new length, and start as zero when they are allocated here.
     """
-    torch = _torch()
-    dev, B, Hkv, ps, mp, npg, d, code = _check_cache(torch, kpages, vpages, kexp, vexp, block_table, seqlens)
-    _is(wacc, "wacc", torch.float32, (B, Hkv, mp * ps), dev)
-    if new_table.dim() != 2:
-        raise ValueError("new_table must be [B, new_max_pages]")
-    nmp = new_table.shape[1]
-    _is(new_table, "new_table", torch.int32, (B, nmp), dev)
-    budget, recent = int(budget), int(recent)
-    if not 1 <= budget <= nmp * ps or not 0 <= recent <= budget:
-        raise ValueError("1 <= budget <= new_max_pages * page_size and 0 <= recent <= budget are wanted")
-    if _elsewhere(torch, dev, stream):
-        with _on(torch, dev, stream):
-            return parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, budget, recent, kexp, vexp,
-                                     new_seqlens, kept, new_wacc)
-    if new_seqlens is None:
-        new_seqlens = torch.empty_like(seqlens)
+    args = (kpages, vpages, kexp, vexp, block_table, seqlens, wacc, new_table, int(budget), int(recent), new_seqlens,
+            kept, new_wacc)
+    if stream is None:
+        r = _native().evict(*args)
     else:
-        _is(new_seqlens, "new_seqlens", torch.int32, (B,), dev)
-    if kept is None:
-        kept = torch.zeros((B, Hkv, budget), dtype=torch.int32, device=dev)
-    else:
-        _is(kept, "kept", torch.int32, (B, Hkv, budget), dev)
-    if new_wacc is None:
-        new_wacc = torch.zeros((B, Hkv, nmp * ps), dtype=torch.float32, device=dev)
-    else:
-        _is(new_wacc, "new_wacc", torch.float32, (B, Hkv, nmp * ps), dev)
-    st = lib().parallax_kv_evict(_at(kpages), _at(vpages), _at(kexp), _at(vexp), _at(block_table), _at(seqlens),
-                                 _at(wacc), _at(new_table), _at(new_seqlens), _at(kept), _at(new_wacc), B, Hkv, ps, mp,
-                                 nmp, npg, d, budget, recent, code, _raw_stream(torch, dev))
-    _check(st, "parallax_kv_evict")
-    return new_seqlens, kept, new_wacc
+        with _on(kpages, stream):
+            r = _native().evict(*args)
+    if type(r) is int:
+        _check(r, "parallax_kv_evict")
+    return r
 
 
 def parallax_rho_proj(x, W_R, H: int, d: int, rho=None, stream=None):

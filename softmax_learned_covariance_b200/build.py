@@ -6,7 +6,8 @@ Each csrc/*.cu is compiled to an object under _build/ (recompiled when it or a
 header changed) and the objects are linked into a shared library next to this
 file.  The CUDA runtime is linked statically so the library loads wherever the
 NVIDIA driver is present; the driver API entry point for TMA descriptors is
-resolved at run time.
+resolved at run time.  csrc/binding.cpp, the native part of the Python binding,
+becomes the extension module _binding.so next to it (g++ against torch's headers).
 """
 from __future__ import annotations
 
@@ -24,6 +25,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libparallax.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -47,6 +50,33 @@ def _stale(src, obj, newest_header):
         return True
     t = os.path.getmtime(obj)
     return os.path.getmtime(src) > t or newest_header > t
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    header = os.path.join(INCLUDE, "parallax.h")
+    if not force and not _stale(BINDING_SRC, BINDING, os.path.getmtime(header)):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], INCLUDE,
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in inc),
+           BINDING_SRC, "-o", tmp, f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           f"-Wl,-rpath,{libs}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        print(r.stdout + r.stderr, file=sys.stderr)
+        raise RuntimeError("g++ failed for: " + BINDING_SRC)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -88,6 +118,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    build_binding(force, verbose)
     return LIB
 
 
