@@ -145,12 +145,16 @@ template <int D, bool Q8, bool RHO, int NT> struct Shape {
     static constexpr int RB = ROW < 128 ? ROW : 128;     // bytes of a box row (and of its swizzle)
     static constexpr int BOXES = ROW / RB;               // boxes of a K or V tile
     static constexpr int HALF = 16 * ROW;                // bytes of a K or V tile
-    static constexpr int TILE_BYTES = 2 * HALF;
-    static constexpr int STAGES = TILE_BYTES <= 2048 ? 4 : 2;            // tiles of a warp's ring
-    // CTAs per SM that registers (128, 168 and 255 a thread) and rings leave room for;
-    // d = 128, e4m3: 4 CTAs of 2 stages against 3 of 4: 256 against 267 us (B=16, 16
-    // heads, 32768 tokens); bf16: 3 of 2 against 4 of 1 or 2 of 3 (160 us each).
-    static constexpr int CTAS = NT == 2 ? 2 : (Q8 || D == 64 ? 4 : 3);
+    static constexpr int SUB_BYTES = 2 * HALF;
+    // 16-token parts of a tile: two, so that a warp has two independent chains of products
+    // and half the work around them (one where two stages of two would leave one CTA per SM)
+    static constexpr int SUBS = Q8 || D == 64 ? 2 : 1;
+    static constexpr int TILE_TOKENS = 16 * SUBS;
+    static constexpr int TILE_BYTES = SUBS * SUB_BYTES;
+    static constexpr int QUAD = WARPS * TILE_TOKENS;     // tokens of one tile per warp: the schedule's step
+    static constexpr int STAGES = TILE_BYTES <= 4096 ? 3 : 2;            // tiles of a warp's ring
+    // CTAs per SM that registers (128, 168 and 255 a thread) and rings leave room for
+    static constexpr int CTAS = NT == 2 ? 2 : (Q8 && D == 64 ? 4 : 3);
     static constexpr int RING_BYTES = WARPS * STAGES * TILE_BYTES;
     static constexpr int BAR_OFF = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
     static constexpr int SMEM = BAR_OFF + 8 * WARPS * STAGES + 1024;     // and what aligning the base to 1024 takes
@@ -198,13 +202,13 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
     if (whole) {                             // one item per CTA
         b = blockIdx.x / per_seq;
         it = blockIdx.x % per_seq;
-        left = quads_of(len_of(b));
+        left = quads_of(len_of(b), S::QUAD);
     } else {
         // prefix sums of the sequences' quads: a run of sequences per thread, then over the threads
         const int run = (B + WARPS * 32 - 1) / (WARPS * 32);
         const int b0 = min((int)threadIdx.x * run, B), b1 = min(b0 + run, B);
         long long own = 0;
-        for (int i = b0; i < b1; ++i) own += quads_of(len_of(i));
+        for (int i = b0; i < b1; ++i) own += quads_of(len_of(i), S::QUAD);
         long long incl = own;
 #pragma unroll
         for (int off = 1; off < 32; off *= 2) {
@@ -231,14 +235,14 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             long long before = incl - own;
             if (before * per_seq <= pos && pos < incl * per_seq) {
                 int i = b0;
-                for (int n; (before + (n = quads_of(len_of(i)))) * per_seq <= pos; ++i) before += n;
+                for (int n; (before + (n = quads_of(len_of(i), S::QUAD))) * per_seq <= pos; ++i) before += n;
                 sh_b = i;
                 sh_before = before;
             }
             __syncthreads();
             b = sh_b;
             const long long rem = pos - sh_before * per_seq;
-            const int n = quads_of(len_of(b));
+            const int n = quads_of(len_of(b), S::QUAD);
             it = (int)(rem / n);
             q0 = (int)(rem % n);
         }
@@ -262,16 +266,16 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
     uint32_t phases = 0;         // parity each stage's barrier completes next
 
     while (true) {
-        const int L = len_of(b), nq = quads_of(L);
+        const int L = len_of(b), nq = quads_of(L, S::QUAD);
         const int q1 = (int)min((long long)nq, q0 + left);
         const int kvh = it / htiles, ht = it % htiles;
         const int g0 = ht * S::HEADS;
         const int nh = min(S::HEADS, pg.group - g0);
         const long h0 = (long)b * Hq + (long)kvh * pg.group + g0;
         const long item = (long)b * per_seq + it;
-        const int t0 = q0 * QUAD;
-        const int t1 = min(L, q1 * QUAD);
-        const int ntiles = (t1 - t0 + 15) / 16;
+        const int t0 = q0 * S::QUAD;
+        const int t1 = min(L, q1 * S::QUAD);
+        const int ntiles = (t1 - t0 + S::TILE_TOKENS - 1) / S::TILE_TOKENS;
         const bool uncut = q0 == 0 && q1 == nq;
 
         float oacc[NT][S::JS][4];
@@ -287,38 +291,52 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         }
         int evref = -1000;        // exponent O and M are held at (e4m3)
 
-        // This warp's tiles are warp + WARPS j.  Lane l holds the page of tile 32 n + l
-        // (a tile's rows share one page: it starts on a multiple of 16 and pages hold at
-        // least 16) and its two exponents, loaded 32 tiles at a time.
+        // This warp's tiles are warp + WARPS j.  Lane l holds the page of its 16-token part
+        // 32 n + l (a part's rows share one page: it starts on a multiple of 16 and pages
+        // hold at least 16) and its two exponents, loaded 32 parts at a time.
         const int mine = ntiles > warp ? (ntiles - warp + WARPS - 1) / WARPS : 0;
-        auto page_of = [&](int j) -> int {
-            return j < mine ? pg.table[(size_t)b * pg.max_pages + ((t0 + (warp + WARPS * j) * 16) >> pg.pshift)] : 0;
+        auto token_of = [&](int part) {
+            return t0 + (warp + WARPS * (part / S::SUBS)) * S::TILE_TOKENS + (part % S::SUBS) * 16;
+        };
+        auto page_of = [&](int part) -> int {
+            const int t = token_of(part);
+            return t < t1 ? pg.table[(size_t)b * pg.max_pages + (t >> pg.pshift)] : 0;
         };
         // exponents of K (low byte) and V (next byte), and BAD for a page id out of range
-        auto info_of = [&](int j, int id) -> int {
-            if (j >= mine) return 0;
+        auto info_of = [&](int part, int id) -> int {
+            const int t = token_of(part);
+            if (t >= t1) return 0;
             if ((unsigned)id >= (unsigned)pg.num_pages) {
                 atomicExch(ctl.err, PARALLAX_ERR_DEVICE_INDEX);
                 return BAD;
             }
             if constexpr (!Q8) return 0;
-            const size_t at = ((size_t)id * pg.Hkv + kvh) * (ps / KV_BLOCK) +
-                              ((t0 + (warp + WARPS * j) * 16) & pmask) / KV_BLOCK;
+            const size_t at = ((size_t)id * pg.Hkv + kvh) * (ps / KV_BLOCK) + (t & pmask) / KV_BLOCK;
             return (kexp[at] & 0xff) | (vexp[at] & 0xff) << 8;
         };
         int ids = page_of(lane), ids_next = 0, info = info_of(lane, ids), info_next = 0;
 
         uint8_t *ring = smem + warp * S::STAGES * S::TILE_BYTES;
-        // loads tile j from page `id` into stage st; the rows of a bad page are not loaded
-        auto issue = [&](int j, int st, int id) {
-            const int t = t0 + (warp + WARPS * j) * 16;
-            const bool ok = (unsigned)id < (unsigned)pg.num_pages;
+        // Loads tile j into stage st; lane l holds the page of part 32 n + l in `pages`.
+        // Parts past the end and those of a bad page are not loaded.
+        auto issue = [&](int j, int st, int pages) {
+            int id[S::SUBS], bytes = 0;
+            bool ok[S::SUBS];
+#pragma unroll
+            for (int u = 0; u < S::SUBS; ++u) {
+                id[u] = __shfl_sync(0xffffffffu, pages, (S::SUBS * j + u) & 31);
+                ok[u] = (unsigned)id[u] < (unsigned)pg.num_pages && token_of(S::SUBS * j + u) < t1;
+                bytes += ok[u] ? S::SUB_BYTES : 0;
+            }
             __syncwarp();                        // every lane has read what the stage held
             if (lane == 0) {
-                mbar_arrive_expect_tx(full + 8 * st, ok ? S::TILE_BYTES : 0);
-                if (ok && !((ctl.debug_flags & DEBUG_DECODE_SKIP_FIRST_TILE) && j == 0)) {
-                    const uint32_t dst = smem_u32(ring + st * S::TILE_BYTES);
-                    const int row = t & pmask, slab = id * pg.Hkv + kvh;
+                mbar_arrive_expect_tx(full + 8 * st, bytes);
+                const bool skip = (ctl.debug_flags & DEBUG_DECODE_SKIP_FIRST_TILE) && j == 0;
+#pragma unroll
+                for (int u = 0; u < S::SUBS; ++u) {
+                    if (!ok[u] || skip) continue;
+                    const uint32_t dst = smem_u32(ring + st * S::TILE_BYTES + u * S::SUB_BYTES);
+                    const int row = token_of(S::SUBS * j + u) & pmask, slab = id[u] * pg.Hkv + kvh;
 #pragma unroll
                     for (int x = 0; x < S::BOXES; ++x) {
                         tma_load_3d(dst + x * 16 * S::RB, &tmk, full + 8 * st, x * (S::RB / S::EL), row, slab);
@@ -328,10 +346,8 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             }
         };
 #pragma unroll
-        for (int j = 0; j < S::STAGES - 1; ++j) {
-            const int id = __shfl_sync(0xffffffffu, ids, j);
-            if (j < mine) issue(j, (stage + j) % S::STAGES, id);
-        }
+        for (int j = 0; j < S::STAGES - 1; ++j)
+            if (j < mine) issue(j, (stage + j) % S::STAGES, ids);
         // ---- the vectors (the first tiles are on their way): column n = r of n-tile nt; 4 elements per MMA step ----
         uint32_t qf[NT][S::KSTEPS][2];
         float zfac[S::HPT], afac[S::HPT];    // of the heads whose state this thread holds
@@ -390,18 +406,26 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         const int vc = S::VB < 16 ? r / 2 : r, vsub = S::VB < 16 ? 8 * (r & 1) : 0;
         const int voff[2] = {S::HALF + chunk_at<S::RB>(va, vc) + vsub, S::HALF + chunk_at<S::RB>(vb, vc) + vsub};
         for (int j = 0; j < mine; ++j) {
-            // ---- pages and exponents of the 32 tiles after these, in good time ----
-            if ((j & 31) == 0)
-                ids_next = page_of(j + 32 + lane);
-            else if ((j & 31) == 16)
-                info_next = info_of(j + 16 + lane, ids_next);
+            // ---- pages and exponents of the 32 parts after these, in good time ----
+            constexpr int PER32 = 32 / S::SUBS;
+            if (j % PER32 == 0)
+                ids_next = page_of(S::SUBS * (j + PER32) + lane);
+            else if (j % PER32 == PER32 / 2)
+                info_next = info_of(S::SUBS * (j + PER32 / 2) + lane, ids_next);
             const int jn = j + S::STAGES - 1;
-            const int id = __shfl_sync(0xffffffffu, (j & 31) + S::STAGES - 1 < 32 ? ids : ids_next, jn & 31);
             // every lane has read the tile before this one: its stage takes tile jn
-            if (jn < mine) issue(jn, stage == 0 ? S::STAGES - 1 : stage - 1, id);
-            const int now = __shfl_sync(0xffffffffu, info, j & 31);
-            const int ke = (int)(signed char)now, ve = (int)(signed char)(now >> 8);
-            if ((j & 31) == 31) {
+            if (jn < mine) issue(jn, stage == 0 ? S::STAGES - 1 : stage - 1, j % PER32 + S::STAGES - 1 < PER32 ? ids : ids_next);
+            int ke[S::SUBS], ve[S::SUBS];
+            bool bad = false;
+#pragma unroll
+            for (int u = 0; u < S::SUBS; ++u) {
+                const int now = __shfl_sync(0xffffffffu, info, (S::SUBS * j + u) & 31);
+                ke[u] = (int)(signed char)now;
+                ve[u] = (int)(signed char)(now >> 8);
+                bad |= (now & BAD) != 0;
+            }
+            const int parts_info = info;
+            if (j % PER32 == PER32 - 1) {
                 ids = ids_next;
                 info = info_next;
             }
@@ -417,67 +441,93 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             phases ^= 1u << stage;
             uint8_t *dk = ring + stage * S::TILE_BYTES;
             stage = stage + 1 == S::STAGES ? 0 : stage + 1;
-            const int tile = t0 + (warp + WARPS * j) * 16;
+            const int tile = token_of(S::SUBS * j);
             const int nvalid = t1 - tile;                   // tokens of the tile
-            if (nvalid < 16 || (now & BAD)) {
-                // rows past the sequence hold whatever the page does, those of a bad page what the
-                // stage held: zeros, as a weight of 0 times NaN is no 0
-                for (int i = lane; i < S::TILE_BYTES / 16; i += 32)
-                    if (i * 16 / S::RB % 16 >= nvalid || (now & BAD)) reinterpret_cast<uint4 *>(dk)[i] = make_uint4(0u, 0u, 0u, 0u);
+            const bool ragged = nvalid < S::TILE_TOKENS;
+            if (ragged || bad) {
+                // rows past the sequence hold whatever the page does, those of a bad page or a part
+                // past the end what the stage held: zeros, as a weight of 0 times NaN is no 0
+#pragma unroll
+                for (int u = 0; u < S::SUBS; ++u) {
+                    const bool out = (__shfl_sync(0xffffffffu, parts_info, (S::SUBS * j + u) & 31) & BAD) != 0;
+                    uint4 *sub = reinterpret_cast<uint4 *>(dk + u * S::SUB_BYTES);
+                    for (int i = lane; i < S::SUB_BYTES / 16; i += 32)
+                        if (out || 16 * u + i * 16 / S::RB % 16 >= nvalid) sub[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
                 fence_proxy_async();               // before a later load into this stage
                 __syncwarp();
             }
 
-            // ---- scores ----
-            float sc[NT][4], sc2[NT][4];          // two chains of products
+            // ---- scores: two chains of products, one per part or by turns ----
+            constexpr int CHAINS = S::SUBS == 1 ? 2 : 1;
+            float sc[S::SUBS][NT][4], sc2[S::SUBS][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < S::SUBS; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][e] = sc2[nt][e] = 0.f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[u][nt][e] = sc2[u][nt][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < S::KC; ++c) {
-                const uint8_t *src = dk + (c / 2) * 16 * S::RB + (koff ^ ((c & 1) << 6));
-                const uint4 k0 = *reinterpret_cast<const uint4 *>(src);
-                const uint4 k1 = *reinterpret_cast<const uint4 *>(src + 8 * S::RB);
-                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+                alignas(16) uint32_t w0[S::SUBS][4], w1[S::SUBS][4];
 #pragma unroll
-                for (int i = 0; i < (Q8 ? 4 : 2); ++i) {
-                    const int st = c * (Q8 ? 4 : 2) + i;
-                    uint32_t a0, a1, a2, a3;
-                    if constexpr (Q8) {
-                        e4m3x4_to_f16x2(w0[i], a0, a2);
-                        e4m3x4_to_f16x2(w1[i], a1, a3);
-                    } else {
-                        a0 = w0[2 * i];
-                        a2 = w0[2 * i + 1];
-                        a1 = w1[2 * i];
-                        a3 = w1[2 * i + 1];
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<Q8>(st % 2 ? sc2[nt] : sc[nt], a0, a1, a2, a3, qf[nt][st][0], qf[nt][st][1]);
+                for (int u = 0; u < S::SUBS; ++u) {
+                    const uint8_t *src = dk + u * S::SUB_BYTES + (c / 2) * 16 * S::RB + (koff ^ ((c & 1) << 6));
+                    *reinterpret_cast<uint4 *>(w0[u]) = *reinterpret_cast<const uint4 *>(src);
+                    *reinterpret_cast<uint4 *>(w1[u]) = *reinterpret_cast<const uint4 *>(src + 8 * S::RB);
                 }
+#pragma unroll
+                for (int i = 0; i < (Q8 ? 4 : 2); ++i)
+#pragma unroll
+                    for (int u = 0; u < S::SUBS; ++u) {
+                        const int st = c * (Q8 ? 4 : 2) + i;
+                        uint32_t a0, a1, a2, a3;
+                        if constexpr (Q8) {
+                            e4m3x4_to_f16x2(w0[u][i], a0, a2);
+                            e4m3x4_to_f16x2(w1[u][i], a1, a3);
+                        } else {
+                            a0 = w0[u][2 * i];
+                            a2 = w0[u][2 * i + 1];
+                            a1 = w1[u][2 * i];
+                            a3 = w1[u][2 * i + 1];
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<Q8>(CHAINS == 2 && st % 2 ? sc2[u][nt] : sc[u][nt], a0, a1, a2, a3, qf[nt][st][0],
+                                         qf[nt][st][1]);
+                    }
             }
+            if constexpr (CHAINS == 2) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][e] += sc2[nt][e];
+                    for (int e = 0; e < 4; ++e) sc[0][nt][e] += sc2[0][nt][e];
+            }
 
             // ---- weights ----
-            float f[S::HPT], dz[S::HPT][2];       // score = sc * f; dz: against the reference
-            bool up = Q8 && ve > evref;
-            const float kscale = Q8 ? exp2_whole(ke) : 1.f;
+            constexpr int ROWS = 2 * S::SUBS;     // a thread's tokens: row x is 16 (x / 2) + (x odd ? tok1 : tok0)
+            auto tok = [&](int x) { return 16 * (x >> 1) + ((x & 1) ? tok1 : tok0); };
+            float f[S::SUBS][S::HPT], dz[S::HPT][ROWS];       // score = sc * f; dz: against the reference
+            float kscale[S::SUBS];
+            bool up = false;
+#pragma unroll
+            for (int u = 0; u < S::SUBS; ++u) {
+                up |= Q8 && ve[u] > evref;
+                kscale[u] = Q8 ? exp2_whole(ke[u]) : 1.f;
+            }
 #pragma unroll
             for (int h = 0; h < S::HPT; ++h) {
                 const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
-                f[h] = Q8 ? fminf(zfac[h] * kscale, 3e38f) : zfac[h];     // finite: a score of 0 stays 0
-                dz[h][0] = fmaf(sc[nt][e], f[h], -mref[h]);
-                dz[h][1] = fmaf(sc[nt][2 + e], f[h], -mref[h]);
-                if (nvalid < 16) {
-                    if (tok0 >= nvalid) dz[h][0] = -INFINITY;
-                    if (tok1 >= nvalid) dz[h][1] = -INFINITY;
+                float top = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < ROWS; ++x) {
+                    const int u = x >> 1;
+                    f[u][h] = Q8 ? fminf(zfac[h] * kscale[u], 3e38f) : zfac[h];     // finite: a score of 0 stays 0
+                    dz[h][x] = fmaf(sc[u][nt][2 * (x & 1) + e], f[u][h], -mref[h]);
+                    if (ragged && tok(x) >= nvalid) dz[h][x] = -INFINITY;
+                    top = fmaxf(top, dz[h][x]);
                 }
-                up |= fmaxf(dz[h][0], dz[h][1]) > HEADROOM;
+                up |= top > HEADROOM;
             }
             if (ws.zs != nullptr) {
                 float *dst = ws.zs + ((size_t)item * Tcap + tile) * S::HEADS;
@@ -485,28 +535,35 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                 for (int h = 0; h < S::HPT; ++h) {
                     const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
                     const int head = RHO ? 4 * h + t4 : 8 * (h / 2) + 2 * t4 + h % 2;
-                    if (tok0 < nvalid) dst[tok0 * S::HEADS + head] = sc[nt][e] * f[h];
-                    if (tok1 < nvalid) dst[tok1 * S::HEADS + head] = sc[nt][2 + e] * f[h];
+#pragma unroll
+                    for (int x = 0; x < ROWS; ++x)
+                        if (tok(x) < nvalid) dst[tok(x) * S::HEADS + head] = sc[x >> 1][nt][2 * (x & 1) + e] * f[x >> 1][h];
                 }
             }
             if (__any_sync(0xffffffffu, up)) {
-                const float vshift = Q8 ? fex2((float)min(evref - ve, 0)) : 1.f;
-                evref = max(evref, ve);
+                int evnew = evref;
+#pragma unroll
+                for (int u = 0; u < S::SUBS; ++u) evnew = Q8 ? max(evnew, ve[u]) : evnew;
+                const float vshift = Q8 ? fex2((float)(evref - evnew)) : 1.f;
+                evref = evnew;
 #pragma unroll
                 for (int h = 0; h < S::HPT; ++h) {
                     const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
-                    float z0 = sc[nt][e] * f[h], z1 = sc[nt][2 + e] * f[h];
-                    if (tok0 >= nvalid) z0 = -INFINITY;
-                    if (tok1 >= nvalid) z1 = -INFINITY;
-                    float mx = fmaxf(z0, z1);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < ROWS; ++x) {
+                        dz[h][x] = sc[x >> 1][nt][2 * (x & 1) + e] * f[x >> 1][h];
+                        if (ragged && tok(x) >= nvalid) dz[h][x] = -INFINITY;
+                        mx = fmaxf(mx, dz[h][x]);
+                    }
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                     const float mnew = fmaxf(mref[h], mx);
                     const float alpha = fex2(mref[h] - mnew);
                     mref[h] = mnew;
-                    dz[h][0] = z0 - mnew;
-                    dz[h][1] = z1 - mnew;
+#pragma unroll
+                    for (int x = 0; x < ROWS; ++x) dz[h][x] -= mnew;
                     lsum[h] *= alpha;
                     asum[h] *= alpha;
                     const float beta = alpha * vshift;
@@ -524,17 +581,18 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                     }
                 }
             }
-            const float vfac = Q8 ? fex2((float)(ve - evref)) : 1.f;
-            uint32_t bh[NT][2], bl[NT][2];    // weights as the value product's operand: hi, lo parts
+            uint32_t bh[NT][ROWS], bl[NT][ROWS];    // weights as the value product's operand: hi, lo parts
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < ROWS; ++x) {
+                const int u = x >> 1;
+                const float vfac = Q8 ? fex2((float)(ve[u] - evref)) : 1.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float w0, w1;
                     if constexpr (RHO) {
                         // masked tokens have p = 0 and, their K rows being zero, a = 0
                         const float p = fex2(dz[nt][x]);
-                        const float a = sc[nt][2 * x + 1] * (Q8 ? fminf(afac[nt] * kscale, 3e38f) : afac[nt]);
+                        const float a = sc[u][nt][2 * (x & 1) + 1] * (Q8 ? fminf(afac[nt] * kscale[u], 3e38f) : afac[nt]);
                         lsum[nt] += p;
                         asum[nt] = fmaf(p, a, asum[nt]);
                         w0 = p * vfac;
@@ -552,24 +610,19 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                     bh[nt][x] = movmatrix(hi);
                     bl[nt][x] = movmatrix(lo);
                 }
+            }
             // ---- O += P V, M += (P o A) V ----
 #pragma unroll
-            for (int c = 0; c < (S::VB + 15) / 16; ++c) {
-                uint32_t v[4][4];
+            for (int cu = 0; cu < (S::VB + 15) / 16 * S::SUBS; ++cu) {
+                const int c = cu / S::SUBS, u = cu % S::SUBS;
+                alignas(16) uint32_t v[4][4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {       // tokens of the weights' columns 2 t4, 2 t4 + 1, + 8, + 9
-                    const uint8_t *src = dk + c * 16 * S::RB + voff[x & 1] + 8 * (x >> 1) * S::RB;
-                    if constexpr (S::VB < 16) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                        v[x][0] = w.x;
-                        v[x][1] = w.y;
-                    } else {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(src);
-                        v[x][0] = w.x;
-                        v[x][1] = w.y;
-                        v[x][2] = w.z;
-                        v[x][3] = w.w;
-                    }
+                    const uint8_t *src = dk + u * S::SUB_BYTES + c * 16 * S::RB + voff[x & 1] + 8 * (x >> 1) * S::RB;
+                    if constexpr (S::VB < 16)
+                        *reinterpret_cast<uint2 *>(v[x]) = *reinterpret_cast<const uint2 *>(src);
+                    else
+                        *reinterpret_cast<uint4 *>(v[x]) = *reinterpret_cast<const uint4 *>(src);
                 }
                 constexpr int PER = S::JS / ((S::VB + 15) / 16);      // MMAs of a chunk
 #pragma unroll
@@ -596,7 +649,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
                                 mma16816<Q8>(oacc[nt][c * PER + g + q4], av[q4][0], av[q4][1], av[q4][2], av[q4][3],
-                                             part ? bl[nt][0] : bh[nt][0], part ? bl[nt][1] : bh[nt][1]);
+                                             part ? bl[nt][2 * u] : bh[nt][2 * u], part ? bl[nt][2 * u + 1] : bh[nt][2 * u + 1]);
                 }
             }
         }
@@ -927,7 +980,7 @@ DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count) 
     const size_t htiles = (A.pg.group + heads - 1) / heads, items = (size_t)A.B * A.pg.Hkv * htiles;
     const size_t cap = (size_t)A.pg.max_pages << A.pg.pshift;
     DecodeCacheScratch s{};
-    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (rho && A.pg.group > 4 ? 2 : (q8 || A.d == 64 ? 4 : 3));
+    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (rho && A.pg.group > 4 ? 2 : (q8 && A.d == 64 ? 4 : 3));
     s.parts = up((size_t)2 * s.ctas * heads * (rho ? 2 : 1) * A.d * sizeof(float));
     s.hdr = up((size_t)2 * s.ctas * heads * sizeof(float4));
     s.cut = up((size_t)s.ctas * sizeof(int2));

@@ -2,7 +2,7 @@
 // plain C++ compiler can check it).
 //
 // An item is one (sequence, KV head, tile of its query heads); its work is the
-// sequence's quads (64 tokens: one 16-token tile for each of a CTA's four warps).
+// sequence's quads (one tile of 16 or 32 tokens for each of a CTA's four warps).
 // All items' quads in a row are cut into equal ranges, one per CTA, whatever the
 // lengths: the lengths are read on the device, so a ragged batch, one long
 // sequence and a table far larger than the sequences all fill the machine.  A
@@ -20,10 +20,9 @@
 
 namespace plx {
 
-constexpr int QUAD = 64;        // tokens
-constexpr int MIN_QUADS = 2;    // of a range, while there are CTAs to spare
+constexpr int MIN_QUADS = 1;    // of a range, while there are CTAs to spare
 
-PLX_HD int quads_of(int tokens) { return (tokens + QUAD - 1) / QUAD; }
+PLX_HD int quads_of(int tokens, int quad) { return (tokens + quad - 1) / quad; }
 
 // CTAs that take part, of `ctas`, for `total` quads
 PLX_HD int sched_ctas(long long total, int ctas) {

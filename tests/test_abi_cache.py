@@ -143,7 +143,7 @@ int main() {
         }
     }
     // the largest batches stay within 64 bits
-    const long long total = (1ll << 36) / QUAD;
+    const long long total = (1ll << 36) / 64;
     return sched_owner(total - 1, total, 592) == 591 && sched_start(592, total, 592) == total ? 0 : 7;
 }
 """)
