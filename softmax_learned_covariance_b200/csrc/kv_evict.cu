@@ -8,8 +8,9 @@
 //
 // Two launches.  k_evict_select finds the weight of the last kept token by a
 // radix select over order-preserving integer keys (three digits of 11, 11 and 10
-// bits) and writes the kept positions in order: a cluster of CTAs per head, whose
-// histograms meet in distributed shared memory; a CTA whose share is at most
+// bits) and writes the kept positions in order: a cluster of CTAs per head, which add
+// the bins they hit to the first one's histogram (reading all histograms in all
+// CTAs took the cluster's shared memories 2 us a digit); a CTA whose share is at most
 // SEL_TILE tokens reads its weights once and keeps the keys in registers.
 // k_evict_move copies the rows, one warp per 16-row destination block (K and V).  An e4m3
 // destination block takes the largest exponent of its rows' source blocks and the
@@ -25,8 +26,9 @@ constexpr int SEL_THREADS = 512;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int SEL_ITEMS = 8;                            // tokens of a thread at a time
 constexpr int SEL_TILE = SEL_THREADS * SEL_ITEMS;
-constexpr int BINS = 2048;
+constexpr int BINS = 2048, OWN = BINS / SEL_THREADS;    // bins, and those a thread sums
 constexpr int MOVE_WARPS = 4;
+static_assert(3 * BINS >= SEL_TILE, "the kept positions of a tile reuse the histograms");
 
 // Weights as integers in the same order: -0 and +0 are equal, NaN is -inf.  The
 // smallest key is 0x007fffff; 0 stands for no token.
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
     };
     __shared__ __align__(16) uint32_t hist[3][BINS];
     __shared__ uint32_t wsum[32];
-    __shared__ uint32_t pick, above, mine[2];
+    __shared__ uint32_t found[2], mine[2];             // a digit and the keys above it; this CTA's counts
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, rank = CLUSTER ? (int)(blockIdx.x % (unsigned)cluster_size) : 0;
     const unsigned bk = blockIdx.x / (unsigned)cluster_size;
@@ -87,18 +89,23 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
     const float *w = A.wacc + (size_t)bk * cap;
     int *kept = A.kept + (size_t)bk * A.budget;
     float *nw = A.new_wacc ? A.new_wacc + bk * ncap : nullptr;
-    for (int i = rank * SEL_THREADS + tid; i < tail; i += cluster_size * SEL_THREADS) {
-        kept[need + i] = C + i;
-        if (nw) nw[need + i] = w[C + i];
+    auto keep_tail = [&] {
+        for (int i = rank * SEL_THREADS + tid; i < tail; i += cluster_size * SEL_THREADS) {
+            kept[need + i] = C + i;
+            if (nw) nw[need + i] = w[C + i];
+        }
+    };
+    if (need == 0) {                                   // the whole cluster
+        keep_tail();
+        return;
     }
-    if (need == 0) return;                             // the whole cluster
     // this CTA's candidates [begin, end)
     const int share = ((C + cluster_size - 1) / cluster_size + 3) & ~3;
     const int begin = min(rank * share, C), end = min(begin + share, C);
     const bool all = need == C, once = share <= SEL_TILE;
 
     uint32_t key[SEL_ITEMS];
-    auto load = [&](int base) {                        // tokens base + 8 tid ..
+    auto load = [&](int base) {                        // tokens base + SEL_ITEMS tid ..
 #pragma unroll
         for (int v = 0; v < SEL_ITEMS; v += 4) {
             const int t = base + SEL_ITEMS * tid + v;
@@ -112,8 +119,8 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
     if (once) load(begin);
     uint32_t prefix = 0, mask = 0, ties = 0;           // the need-th largest key, found from the top bits down
     if (!all) {
-        for (int i = tid; i < 3 * BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0u;
-        __syncthreads();
+        for (int i = tid; i < 3 * BINS / 4; i += SEL_THREADS) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+        sync();                                        // zero before any CTA of the cluster adds to it
         uint32_t left = (uint32_t)need;                // how many of the keys that match `prefix` are wanted
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
@@ -126,38 +133,55 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
                     if ((k & mask) == prefix && k != 0u) atomicAdd(&hist[pass][(k >> shift) & digit], 1u);
                 }
             }
-            sync();                                    // every CTA's histogram of this digit is complete
-            // thread i owns bins 2047 - 4 i .. 2044 - 4 i: an exclusive sum from the largest bin down
-            uint4 h = make_uint4(0u, 0u, 0u, 0u);
+            __syncthreads();                           // this CTA's histogram of the digit is complete
+            // thread i owns the OWN bins below BINS - OWN i
+            const int top = BINS - OWN * (tid + 1);
+            uint32_t h[OWN];
+            auto read = [&] {
 #pragma unroll
-            for (int q = 0; q < (CLUSTER ? 8 : 1); ++q) {
-                if (q >= cluster_size) break;
-                const uint32_t *theirs = CLUSTER ? cluster.map_shared_rank(&hist[pass][0], q) : &hist[pass][0];
-                const uint4 o = *reinterpret_cast<const uint4 *>(theirs + BINS - 4 - 4 * tid);
-                h.x += o.x;
-                h.y += o.y;
-                h.z += o.z;
-                h.w += o.w;
-            }
-            uint32_t total;
-            uint32_t before = block_scan(h.x + h.y + h.z + h.w, wsum, total);
-            const uint32_t down[4] = {h.w, h.z, h.y, h.x};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (before < left && left <= before + down[i]) {
-                    pick = (uint32_t)(BINS - 1 - 4 * tid - i);
-                    above = before;
+                for (int i = 0; i < OWN; i += 4) {
+                    const uint4 o = *reinterpret_cast<const uint4 *>(&hist[pass][top + i]);
+                    h[i] = o.x;
+                    h[i + 1] = o.y;
+                    h[i + 2] = o.z;
+                    h[i + 3] = o.w;
                 }
-                before += down[i];
+            };
+            read();
+            if constexpr (CLUSTER) {
+                if (rank != 0) {
+                    uint32_t *first = cluster.map_shared_rank(&hist[pass][top], 0);
+#pragma unroll
+                    for (int i = 0; i < OWN; ++i)
+                        if (h[i]) atomicAdd(first + i, h[i]);
+                }
+                cluster.sync();
+                read();
             }
-            __syncthreads();
-            prefix |= pick << shift;
+            if (rank == 0) {
+                // an exclusive sum from the largest bin down finds the bin of the last wanted key
+                uint32_t total, own = 0;
+#pragma unroll
+                for (int i = 0; i < OWN; ++i) own += h[i];
+                uint32_t before = block_scan(own, wsum, total);
+                if (before < left && left <= before + own) {
+                    int i = OWN - 1;
+                    for (; i > 0 && before + hist[pass][top + i] < left; --i) before += hist[pass][top + i];
+                    for (int q = 0; q < cluster_size; ++q) {
+                        uint32_t *to = CLUSTER ? cluster.map_shared_rank(found, q) : found;
+                        to[0] = (uint32_t)(top + i);
+                        to[1] = before;
+                    }
+                }
+            }
+            sync();
+            prefix |= found[0] << shift;
             mask |= digit << shift;
-            left -= above;
+            left -= found[1];
         }
         ties = left;                                   // this many of the tokens whose key is `prefix`, in order
     }
-    // Larger keys (low half: at most 8 per thread of 512) and equal ones (high half) of a
+    // Larger keys (low half: at most SEL_TILE of a CTA) and equal ones (high half) of a
     // thread's tokens; when all are kept, prefix and ties are 0.
     auto count = [&] {
         uint32_t c = 0;
@@ -186,27 +210,34 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
             tied += theirs[1];
         }
     }
-    // ---- kept positions in order ----
+    // ---- kept positions in order, through shared memory: a thread's are not next to its
+    // neighbours' (stored one by one, the 4-byte writes took half of the kernel's time) ----
+    int *staged = reinterpret_cast<int *>(hist);       // SEL_TILE of them; the histograms are done
     for (int base = begin; base < end; base += SEL_TILE) {
         if (!once) load(base);
         uint32_t total;
         const uint32_t sc = block_scan(count(), wsum, total);
+        const uint32_t from = larger + min(tied, ties);
         uint32_t g = larger + (sc & 0xffffu), e = tied + (sc >> 16);
 #pragma unroll
         for (int i = 0; i < SEL_ITEMS; ++i) {
             const bool gt = key[i] > prefix, eq = key[i] == prefix;
-            if (gt || (eq && e < ties)) {
-                const int t = base + SEL_ITEMS * tid + i;
-                const uint32_t at = g + min(e, ties);
-                kept[at] = t;
-                if (nw) nw[at] = w[t];
-            }
+            if (gt || (eq && e < ties)) staged[g + min(e, ties) - from] = base + SEL_ITEMS * tid + i;
             g += gt;
             e += eq;
         }
         larger += total & 0xffffu;
         tied += total >> 16;
+        __syncthreads();
+        const uint32_t n_here = larger + min(tied, ties) - from;
+        for (uint32_t i = tid; i < n_here; i += SEL_THREADS) {
+            const int t = staged[i];
+            kept[from + i] = t;
+            if (nw) nw[from + i] = w[t];
+        }
+        __syncthreads();
     }
+    keep_tail();
     if constexpr (CLUSTER) cluster.sync();             // no CTA leaves while its counts are read
 }
 
