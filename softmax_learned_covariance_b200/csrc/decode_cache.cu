@@ -144,13 +144,13 @@ template <int D, bool Q8, bool RHO, int NT> struct Shape {
     static constexpr int MERGE_BYTES = WARPS * HEADS * MSTRIDE * 4;
     static constexpr int RB = ROW < 128 ? ROW : 128;     // bytes of a box row (and of its swizzle)
     static constexpr int BOXES = ROW / RB;               // boxes of a K or V tile
-    static constexpr int HALF = 16 * ROW;                // bytes of a K or V tile
-    static constexpr int SUB_BYTES = 2 * HALF;
+    static constexpr int PART = 16 * ROW;                // bytes of 16 tokens of K or V
     // 16-token parts of a tile: two, so that a warp has two independent chains of products
     // and half the work around them (one where two stages of two would leave one CTA per SM)
     static constexpr int SUBS = Q8 || D == 64 ? 2 : 1;
     static constexpr int TILE_TOKENS = 16 * SUBS;
-    static constexpr int TILE_BYTES = SUBS * SUB_BYTES;
+    static constexpr int HALF = SUBS * PART;             // bytes of a K or V tile
+    static constexpr int TILE_BYTES = 2 * HALF;
     static constexpr int QUAD = WARPS * TILE_TOKENS;     // tokens of one tile per warp: the schedule's step
     static constexpr int STAGES = TILE_BYTES <= 4096 ? 3 : 2;            // tiles of a warp's ring
     // CTAs per SM that registers (128, 168 and 255 a thread) and rings leave room for
@@ -326,16 +326,16 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             for (int u = 0; u < S::SUBS; ++u) {
                 id[u] = __shfl_sync(0xffffffffu, pages, (S::SUBS * j + u) & 31);
                 ok[u] = (unsigned)id[u] < (unsigned)pg.num_pages && token_of(S::SUBS * j + u) < t1;
-                bytes += ok[u] ? S::SUB_BYTES : 0;
+                bytes += ok[u] ? 2 * S::PART : 0;
             }
             __syncwarp();                        // every lane has read what the stage held
             if (lane == 0) {
-                mbar_arrive_expect_tx(full + 8 * st, bytes);
                 const bool skip = (ctl.debug_flags & DEBUG_DECODE_SKIP_FIRST_TILE) && j == 0;
+                mbar_arrive_expect_tx(full + 8 * st, bytes);
 #pragma unroll
                 for (int u = 0; u < S::SUBS; ++u) {
                     if (!ok[u] || skip) continue;
-                    const uint32_t dst = smem_u32(ring + st * S::TILE_BYTES + u * S::SUB_BYTES);
+                    const uint32_t dst = smem_u32(ring + st * S::TILE_BYTES + u * S::PART);
                     const int row = token_of(S::SUBS * j + u) & pmask, slab = id[u] * pg.Hkv + kvh;
 #pragma unroll
                     for (int x = 0; x < S::BOXES; ++x) {
@@ -450,9 +450,11 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
 #pragma unroll
                 for (int u = 0; u < S::SUBS; ++u) {
                     const bool out = (__shfl_sync(0xffffffffu, parts_info, (S::SUBS * j + u) & 31) & BAD) != 0;
-                    uint4 *sub = reinterpret_cast<uint4 *>(dk + u * S::SUB_BYTES);
-                    for (int i = lane; i < S::SUB_BYTES / 16; i += 32)
-                        if (out || 16 * u + i * 16 / S::RB % 16 >= nvalid) sub[i] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = lane; i < 2 * S::PART / 16; i += 32) {
+                        const int kv = i / (S::PART / 16), at = i % (S::PART / 16) * 16;      // K or V, byte of the part
+                        if (out || 16 * u + at / S::RB % 16 >= nvalid)
+                            *reinterpret_cast<uint4 *>(dk + kv * S::HALF + u * S::PART + at) = make_uint4(0u, 0u, 0u, 0u);
+                    }
                 }
                 fence_proxy_async();               // before a later load into this stage
                 __syncwarp();
@@ -472,7 +474,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                 alignas(16) uint32_t w0[S::SUBS][4], w1[S::SUBS][4];
 #pragma unroll
                 for (int u = 0; u < S::SUBS; ++u) {
-                    const uint8_t *src = dk + u * S::SUB_BYTES + (c / 2) * 16 * S::RB + (koff ^ ((c & 1) << 6));
+                    const uint8_t *src = dk + u * S::PART + (c / 2) * 16 * S::RB + (koff ^ ((c & 1) << 6));
                     *reinterpret_cast<uint4 *>(w0[u]) = *reinterpret_cast<const uint4 *>(src);
                     *reinterpret_cast<uint4 *>(w1[u]) = *reinterpret_cast<const uint4 *>(src + 8 * S::RB);
                 }
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                 alignas(16) uint32_t v[4][4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {       // tokens of the weights' columns 2 t4, 2 t4 + 1, + 8, + 9
-                    const uint8_t *src = dk + u * S::SUB_BYTES + c * 16 * S::RB + voff[x & 1] + 8 * (x >> 1) * S::RB;
+                    const uint8_t *src = dk + u * S::PART + c * 16 * S::RB + voff[x & 1] + 8 * (x >> 1) * S::RB;
                     if constexpr (S::VB < 16)
                         *reinterpret_cast<uint2 *>(v[x]) = *reinterpret_cast<const uint2 *>(src);
                     else
@@ -753,18 +755,27 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
 // and head; the others add the weights s = 2^(z - lse2) of ACC_TOKENS tokens of
 // one (b, kvh) to the accumulator, summed over the KV head's query heads in head
 // order (each token by one thread: the result does not depend on the schedule).
+// n / d for n < 2^31 by a multiplication (d >= 1): m = ceil(2^(31 + s) / d) with 2^s >= d.
+struct Divisor {
+    unsigned d, m, s;
+    explicit Divisor(int n) : d(n > 0 ? (unsigned)n : 1u), s(0) {
+        while ((1ull << s) < d) ++s;
+        m = (unsigned)(((1ull << (31 + s)) + d - 1) / d);
+    }
+    __device__ __forceinline__ unsigned of(unsigned n) const { return (unsigned)(((unsigned long long)n * m) >> (31 + s)); }
+};
 constexpr int FIN_THREADS = 256;
 constexpr int ACC_TOKENS = 1024;
 
 template <int D, bool RHO, int HEADS, typename Tout>
-__global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
+__global__ void __launch_bounds__(FIN_THREADS, 4) k_decode_finish(
     Scratch ws, const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse, float *__restrict__ wacc,
-    int Hq, int Hkv, int htiles, int Tcap, int ctas, int hpb, int combine_blocks, int acc_chunks) {
+    int Hq, int Hkv, int htiles, int Tcap, int ctas, int hpb, int combine_blocks, Divisor by_chunks, Divisor by_heads) {
     constexpr int COLS = (RHO ? 2 : 1) * D / 4;               // float4 columns of a part
     constexpr int GROUPS = FIN_THREADS / COLS;                // thread groups of one column each
     __shared__ float4 red[GROUPS][COLS];
-    __shared__ float2 redl[GROUPS];
-    __shared__ float slse[HEADS];
+    __shared__ float4 redl[GROUPS];
+    __shared__ __align__(16) float slse[HEADS];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int group = Hq / Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -797,43 +808,63 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
             const bool live = hh < hfirst + hpb && g0 + hh < group;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             float l = 0.f, ab = 0.f, mu = MNONE;
-            if (live) {                                       // a group is whole warps, so is `live`
-                for (int s = lane; s < nv; s += 32) mu = fmaxf(mu, ws.hdr[sched_part(c0, s) * HEADS + hh].x);
-#pragma unroll
-                for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
+            if (live) {
+                // header and part of four parts at a time, against the group's own maximum so far
                 const float4 *P = reinterpret_cast<const float4 *>(ws.parts) + col;
-#pragma unroll 4
-                for (int s = grp % by; s < nv; s += by) {
-                    const int slot = sched_part(c0, s) * HEADS + hh;
-                    const float4 h = ws.hdr[slot];
-                    const float4 p = P[(size_t)slot * COLS];
-                    const float w = fex2(h.x - mu);
-                    l = fmaf(w, h.y, l);
-                    ab = fmaf(w, h.z, ab);
-                    acc.x = fmaf(w, p.x, acc.x);
-                    acc.y = fmaf(w, p.y, acc.y);
-                    acc.z = fmaf(w, p.z, acc.z);
-                    acc.w = fmaf(w, p.w, acc.w);
+                for (int s0 = grp % by; s0 < nv; s0 += 4 * by) {
+                    float4 h[4], p[4];
+                    float top = mu;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int s = s0 + i * by;
+                        const int slot = sched_part(c0, s < nv ? s : s0) * HEADS + hh;
+                        h[i] = ws.hdr[slot];
+                        p[i] = P[(size_t)slot * COLS];
+                        if (s >= nv) h[i].x = -INFINITY;       // weighs 0
+                        top = fmaxf(top, h[i].x);
+                    }
+                    const float down = fex2(mu - top);
+                    mu = top;
+                    l *= down;
+                    ab *= down;
+                    acc = make_float4(acc.x * down, acc.y * down, acc.z * down, acc.w * down);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = fex2(h[i].x - mu);
+                        l = fmaf(w, h[i].y, l);
+                        ab = fmaf(w, h[i].z, ab);
+                        acc.x = fmaf(w, p[i].x, acc.x);
+                        acc.y = fmaf(w, p[i].y, acc.y);
+                        acc.z = fmaf(w, p[i].z, acc.z);
+                        acc.w = fmaf(w, p[i].w, acc.w);
+                    }
                 }
             }
             __syncthreads();
             red[grp][col] = acc;
-            if (col == 0) redl[grp] = make_float2(l, ab);
+            if (col == 0) redl[grp] = make_float4(l, ab, mu, 0.f);
             __syncthreads();
             if (live) {
                 const int first = grp / by * by;              // the groups of this head
+                for (int i = 0; i < by; ++i) mu = fmaxf(mu, redl[first + i].z);
+                float w[GROUPS];
                 l = ab = 0.f;
-                for (int i = 0; i < by; ++i) {
-                    l += redl[first + i].x;
-                    ab += redl[first + i].y;
+#pragma unroll
+                for (int i = 0; i < GROUPS; ++i) {
+                    if (i >= by) break;
+                    w[i] = fex2(redl[first + i].z - mu);
+                    l = fmaf(w[i], redl[first + i].x, l);
+                    ab = fmaf(w[i], redl[first + i].y, ab);
                 }
                 const float inv = 1.f / l;
                 const float *R = reinterpret_cast<const float *>(red[first]);
                 for (int e = tid - first * COLS; e < D; e += by * COLS) {
                     float o = 0.f, m = 0.f;
-                    for (int i = 0; i < by; ++i) {
-                        o += R[i * COLS * 4 + e];
-                        if constexpr (RHO) m += R[i * COLS * 4 + D + e];
+#pragma unroll
+                    for (int i = 0; i < GROUPS; ++i) {
+                        if (i >= by) break;
+                        o = fmaf(w[i], R[i * COLS * 4 + e], o);
+                        if constexpr (RHO) m = fmaf(w[i], R[i * COLS * 4 + D + e], m);
                     }
                     float out = o * inv;
                     if constexpr (RHO) out -= m * inv - out * (ab * inv);
@@ -846,70 +877,87 @@ __global__ void __launch_bounds__(FIN_THREADS) k_decode_finish(
     }
     // ---- accumulate: every load whose address is known is issued first ----
     const unsigned rest = blockIdx.x - combine_blocks;
-    const int t0 = (int)(rest % (unsigned)acc_chunks) * ACC_TOKENS;
-    const unsigned bk = rest / (unsigned)acc_chunks;           // b * Hkv + kvh
-    const int b = (int)(bk / (unsigned)Hkv), kvh = (int)(bk % (unsigned)Hkv);
+    const unsigned bk = by_chunks.of(rest);                    // b * Hkv + kvh
+    const int t0 = (int)(rest - bk * by_chunks.d) * ACC_TOKENS;
+    const int b = (int)by_heads.of(bk), kvh = (int)(bk - (unsigned)b * Hkv);
     constexpr int PER = ACC_TOKENS / FIN_THREADS;
     const int L = min(max(seqlens[b], 0), Tcap);
-    float sum[PER], had[PER];
+    const size_t row = (size_t)bk * Tcap + t0 + tid;
+    float *W = wacc + row;
+    float sum[PER], add[PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int t = t0 + tid + k * FIN_THREADS;
-        sum[k] = 0.f;
-        had[k] = t < Tcap ? wacc[(size_t)bk * Tcap + t] : 0.f;
-    }
-    for (int ht = 0; ht < htiles; ++ht) {
-        const int nh = min(HEADS, group - ht * HEADS);
-        const int item = (int)bk * htiles + ht;
-        const long h0 = (long)b * Hq + (long)kvh * group + ht * HEADS;
-        float4 z[PER][HEADS / 4];
+    for (int k = 0; k < PER; ++k) add[k] = 0.f;
+    // `full`: no token of the chunk lies past the table (their scratch and weights may be
+    // read, also past the sequence's end, but only tokens before it are written)
+    auto run = [&](auto full_, auto htiles_) {
+        constexpr bool FULL = decltype(full_)::value;
+        const int nht = decltype(htiles_)::value ? 1 : htiles;
+        const int room = Tcap - t0 - tid;
 #pragma unroll
-        for (int k = 0; k < PER; ++k)
+        for (int k = 0; k < PER; ++k) sum[k] = FULL || k * FIN_THREADS < room ? W[k * FIN_THREADS] : 0.f;
+        for (int ht = 0; ht < nht; ++ht) {
+            const int nh = min(HEADS, group - ht * HEADS);
+            const int item = (int)bk * nht + ht;
+            const long h0 = (long)b * Hq + (long)kvh * group + ht * HEADS;
+            const float4 *Z = reinterpret_cast<const float4 *>(ws.zs) +
+                              ((size_t)item * Tcap + t0 + tid) * (HEADS / 4);
+            float4 z[PER][HEADS / 4];
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+#pragma unroll
+                for (int c = 0; c < HEADS / 4; ++c)
+                    z[k][c] = FULL || k * FIN_THREADS < room ? Z[k * FIN_THREADS * (HEADS / 4) + c]
+                                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            int2 info = ws.item[item];
+            const float l2 = lane < nh ? ws.lse2[h0 + lane] : 0.f;       // of an uncut item
+            if (t0 >= L) return;
+            // a decode that gave up on a wait has not written it: whatever is read stays in bounds
+            if (info.x < 0 || info.x >= ctas || info.y < 1 || info.y > ctas - info.x) info = make_int2(0, 1);
+            if (ht > 0) __syncthreads();
+            if (info.y == 1) {
+                if (tid < nh) slse[tid] = l2;
+            } else {
+                for (int h = warp; h < nh; h += FIN_THREADS / 32) {
+                    float top = MNONE, l = 0.f;
+                    for (int s = lane; s < info.y; s += 32) {
+                        const float4 p = ws.hdr[sched_part(info.x, s) * HEADS + h];
+                        const float m = fmaxf(top, p.x);
+                        l = l * fex2(top - m) + fex2(p.x - m) * p.y;
+                        top = m;
+                    }
+                    float mu = top;
+#pragma unroll
+                    for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
+                    l *= fex2(top - mu);
+#pragma unroll
+                    for (int off = 16; off > 0; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
+                    if (lane == 0) slse[h] = mu + log2f(l);
+                }
+            }
+            __syncthreads();
 #pragma unroll
             for (int c = 0; c < HEADS / 4; ++c) {
-                const int t = t0 + tid + k * FIN_THREADS;
-                z[k][c] = t < Tcap ? reinterpret_cast<const float4 *>(ws.zs + ((size_t)item * Tcap + t) * HEADS)[c]
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        int2 info = ws.item[item];
-        float l2 = lane < nh ? ws.lse2[h0 + lane] : 0.f;       // of an uncut item
-        if (t0 >= L) return;
-        // a decode that gave up on a wait has not written it: whatever is read stays in bounds
-        if (info.x < 0 || info.x >= ctas || info.y < 1 || info.y > ctas - info.x) info = make_int2(0, 1);
-        __syncthreads();
-        if (info.y == 1) {
-            if (tid < nh) slse[tid] = l2;
-        } else {
-            for (int h = warp; h < nh; h += FIN_THREADS / 32) {
-                float mu = MNONE, l = 0.f;
-                for (int s = lane; s < info.y; s += 32) mu = fmaxf(mu, ws.hdr[sched_part(info.x, s) * HEADS + h].x);
+                const float4 ls = *reinterpret_cast<const float4 *>(&slse[4 * c]);
+                const int live = nh - 4 * c;       // of these four heads; the others' scores are not looked at
 #pragma unroll
-                for (int off = 16; off > 0; off /= 2) mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, off));
-                for (int s = lane; s < info.y; s += 32) {
-                    const float4 p = ws.hdr[sched_part(info.x, s) * HEADS + h];
-                    l += fex2(p.x - mu) * p.y;
+                for (int k = 0; k < PER; ++k) {
+                    const float w0 = live > 0 ? fex2(z[k][c].x - ls.x) : 0.f, w1 = live > 1 ? fex2(z[k][c].y - ls.y) : 0.f,
+                                w2 = live > 2 ? fex2(z[k][c].z - ls.z) : 0.f, w3 = live > 3 ? fex2(z[k][c].w - ls.w) : 0.f;
+                    add[k] += ((w0 + w1) + w2) + w3;
                 }
-#pragma unroll
-                for (int off = 16; off > 0; off /= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
-                if (lane == 0) slse[h] = mu + log2f(l);
             }
         }
-        __syncthreads();
 #pragma unroll
         for (int k = 0; k < PER; ++k)
-#pragma unroll
-            for (int c = 0; c < HEADS / 4; ++c) {
-                const float zv[4] = {z[k][c].x, z[k][c].y, z[k][c].z, z[k][c].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * c + i < nh) sum[k] += fex2(zv[i] - slse[4 * c + i]);
-            }
-    }
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int t = t0 + tid + k * FIN_THREADS;
-        if (t < L) wacc[(size_t)bk * Tcap + t] = had[k] + sum[k];
-    }
+            if (t0 + tid + k * FIN_THREADS < L) W[k * FIN_THREADS] = sum[k] + add[k];
+    };
+    using yes = std::true_type;
+    using no = std::false_type;
+    const bool full = t0 + ACC_TOKENS <= Tcap;
+    if (htiles == 1)
+        full ? run(yes{}, yes{}) : run(no{}, yes{});
+    else
+        full ? run(yes{}, no{}) : run(no{}, no{});
 }
 
 template <int D, bool Q8, bool RHO, int NT, typename Tout>
@@ -954,7 +1002,8 @@ cudaError_t launch_t(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, voi
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k_decode_finish<D, RHO, S::HEADS, Tout>, ws, A.seqlens, (Tout *)A.y, A.lse, A.wacc,
-                              A.Hq, A.pg.Hkv, htiles, Tcap, whole ? 1 : sc.ctas, hpb, combine, acc_chunks);
+                              A.Hq, A.pg.Hkv, htiles, Tcap, whole ? 1 : sc.ctas, hpb, combine, Divisor(acc_chunks),
+                              Divisor(A.pg.Hkv));
 }
 
 template <int D, bool Q8, typename Tout>

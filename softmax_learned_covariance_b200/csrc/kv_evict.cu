@@ -230,10 +230,11 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
         tied += total >> 16;
         __syncthreads();
         const uint32_t n_here = larger + min(tied, ties) - from;
-        for (uint32_t i = tid; i < n_here; i += SEL_THREADS) {
-            const int t = staged[i];
-            kept[from + i] = t;
-            if (nw) nw[from + i] = w[t];
+#pragma unroll 4
+        for (uint32_t i = tid; i < n_here; i += SEL_THREADS) kept[from + i] = staged[i];
+        if (nw) {
+#pragma unroll 4
+            for (uint32_t i = tid; i < n_here; i += SEL_THREADS) nw[from + i] = w[staged[i]];
         }
         __syncthreads();
     }
