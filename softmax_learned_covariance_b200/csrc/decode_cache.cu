@@ -112,7 +112,10 @@ template <> __device__ __forceinline__ void store_y<__nv_bfloat16>(__nv_bfloat16
     *p = __float2bfloat16_rn(v);
 }
 
-constexpr int BAD = 1 << 16;     // a tile's page id is out of range
+constexpr int BAD = 1 << 16;     // a part's page id is out of range
+// Exponents (-128, -128) of a part that is not there: below any other, so that it
+// never sets the exponent O and M are held at.
+constexpr int NO_EXPONENTS = 0x8080;
 
 // Token of row i < 8 of the products' 16-row operand (row i + 8: the token + 8).
 // A shared-memory phase is 8 threads of 16 bytes, rows 2 m and 2 m + 1 by four chunks
@@ -154,7 +157,7 @@ template <int D, bool Q8, bool RHO, int NT> struct Shape {
     static constexpr int QUAD = WARPS * TILE_TOKENS;     // tokens of one tile per warp: the schedule's step
     static constexpr int STAGES = TILE_BYTES <= 4096 ? 3 : 2;            // tiles of a warp's ring
     // CTAs per SM that registers (128, 168 and 255 a thread) and rings leave room for
-    static constexpr int CTAS = NT == 2 ? 2 : (Q8 && D == 64 ? 4 : 3);
+    static constexpr int CTAS = NT == 2 && D == 128 ? 2 : (NT == 1 && Q8 && D == 64 ? 4 : 3);
     static constexpr int RING_BYTES = WARPS * STAGES * TILE_BYTES;
     static constexpr int BAR_OFF = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
     static constexpr int SMEM = BAR_OFF + 8 * WARPS * STAGES + 1024;     // and what aligning the base to 1024 takes
@@ -208,6 +211,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         const int run = (B + WARPS * 32 - 1) / (WARPS * 32);
         const int b0 = min((int)threadIdx.x * run, B), b1 = min(b0 + run, B);
         long long own = 0;
+#pragma unroll 8
         for (int i = b0; i < b1; ++i) own += quads_of(len_of(i), S::QUAD);
         long long incl = own;
 #pragma unroll
@@ -305,10 +309,10 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         // exponents of K (low byte) and V (next byte), and BAD for a page id out of range
         auto info_of = [&](int part, int id) -> int {
             const int t = token_of(part);
-            if (t >= t1) return 0;
+            if (t >= t1) return NO_EXPONENTS;
             if ((unsigned)id >= (unsigned)pg.num_pages) {
                 atomicExch(ctl.err, PARALLAX_ERR_DEVICE_INDEX);
-                return BAD;
+                return BAD | NO_EXPONENTS;
             }
             if constexpr (!Q8) return 0;
             const size_t at = ((size_t)id * pg.Hkv + kvh) * (ps / KV_BLOCK) + (t & pmask) / KV_BLOCK;
@@ -1029,7 +1033,8 @@ DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count) 
     const size_t htiles = (A.pg.group + heads - 1) / heads, items = (size_t)A.B * A.pg.Hkv * htiles;
     const size_t cap = (size_t)A.pg.max_pages << A.pg.pshift;
     DecodeCacheScratch s{};
-    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (rho && A.pg.group > 4 ? 2 : (q8 && A.d == 64 ? 4 : 3));
+    const bool two = rho && A.pg.group > 4;      // as Shape::CTAS
+    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (two && A.d == 128 ? 2 : (!two && q8 && A.d == 64 ? 4 : 3));
     s.parts = up((size_t)2 * s.ctas * heads * (rho ? 2 : 1) * A.d * sizeof(float));
     s.hdr = up((size_t)2 * s.ctas * heads * sizeof(float4));
     s.cut = up((size_t)s.ctas * sizeof(int2));
