@@ -319,6 +319,8 @@ _bound = None
 def _native():
     """The native part of the binding (csrc/binding.cpp) with the loaded library's entry points."""
     global _bound
+    if _bound is not None and _bound is _lib:
+        return _native.module
     L = lib()
     if _bound is not L:
         _torch()

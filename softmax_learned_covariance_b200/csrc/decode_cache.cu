@@ -199,6 +199,10 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
     auto len_of = [&](int i) { return min(max(seqlens[i], 0), Tcap); };
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
     // ---- this CTA's range of quads: from quad `q0` of item `it` of sequence `b`, `left` quads ----
     int b, it, q0 = 0, cta = 0, nctas = 1;
     long long left, pos = 0, total = 1;
@@ -247,8 +251,8 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             b = sh_b;
             const long long rem = pos - sh_before * per_seq;
             const int n = quads_of(len_of(b), S::QUAD);
-            it = (int)(rem / n);
-            q0 = (int)(rem % n);
+            it = (int)sched_div(rem, n);
+            q0 = (int)(rem - (long long)it * n);
         }
     }
     // sequences without a token: nothing else writes their rows

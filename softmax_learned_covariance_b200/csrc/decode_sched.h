@@ -29,10 +29,14 @@ PLX_HD int sched_ctas(long long total, int ctas) {
     const long long n = (total + MIN_QUADS - 1) / MIN_QUADS;
     return n < ctas ? (int)n : ctas;
 }
+// a / b, in 32 bits where they suffice (a 64-bit division takes the GPU some hundred cycles)
+PLX_HD long long sched_div(long long a, long long b) {
+    return a <= 0x7fffffff && b <= 0x7fffffff ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 // first quad of CTA c's range
-PLX_HD long long sched_start(int c, long long total, int n) { return (long long)c * total / n; }
+PLX_HD long long sched_start(int c, long long total, int n) { return sched_div((long long)c * total, n); }
 // the CTA whose range holds quad x
-PLX_HD int sched_owner(long long x, long long total, int n) { return (int)(((x + 1) * n - 1) / total); }
+PLX_HD int sched_owner(long long x, long long total, int n) { return (int)sched_div((x + 1) * n - 1, total); }
 // slot of the part of an item that CTA c holds
 PLX_HD int sched_slot(int c, bool from_start) { return 2 * c + (from_start ? 1 : 0); }
 // slot of part i of an item whose first CTA is c0
