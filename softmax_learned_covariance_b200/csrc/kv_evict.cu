@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
             tied += theirs[1];
         }
     }
-    // ---- kept positions in order, through shared memory: a thread's are not next to its
-    // neighbours' (stored one by one, the 4-byte writes took half of the kernel's time) ----
+    // ---- kept positions in order, through shared memory, so that whole lines are stored
+    // (one by one: 20 against 18.5 us for 512 heads of 4096) ----
     int *staged = reinterpret_cast<int *>(hist);       // SEL_TILE of them; the histograms are done
     for (int base = begin; base < end; base += SEL_TILE) {
         if (!once) load(base);
