@@ -16,19 +16,22 @@
 // a (token, head) in one thread, and one movmatrix per 8 tokens turns the
 // weights into the second product's operand.
 //
-// Each warp streams its own 16-token tiles through a ring in shared memory that
-// TMA fills, one box of 16 rows each for K and V (two for 256-byte rows).  The
-// order of the contracted index is free as long as both operands agree, so a
-// thread reads whole 16-byte chunks and uses them as its part of the fragments
-// (K: chunks of its own two tokens; V: the same chunk of its four tokens): no
-// ldmatrix, and no barrier beyond the warp's own mbarriers.  The order of the
-// tokens is free too; with the hardware's swizzle it is chosen so that no read
-// has a bank conflict (row_of).
-// The loads bound the kernel and how they are issued decides their rate (B=64,
-// 16 heads of their own, 4096 tokens, d = 128, 1.07 GB; loads alone): 16-byte
-// cp.async in fragment order 205 us, in row order 196 us, bulk copies 168 us;
-// bulk copies of padded four-row pieces cost the warps 10 us more to issue than
-// whole tiles.
+// Each warp streams its own tiles of 32 tokens (16 of 256-byte rows) through a ring
+// in shared memory that TMA fills, one box of 16 rows each for K and V (two for
+// 256-byte rows).  The order of the contracted index is free as long as both
+// operands agree, so a thread reads whole 16-byte chunks and uses them as its part
+// of the fragments (K: chunks of its own two tokens; V: the same chunk of its four
+// tokens): no ldmatrix, and no barrier beyond the warp's own mbarriers.  The order
+// of the tokens is free too; with the hardware's swizzle it is chosen so that no
+// read has a bank conflict (row_of).
+//
+// Bound by the loads, and how they are issued decides their rate (B=64, 16 heads of
+// their own, 4096 tokens, d = 128, 1.07 GB; loads alone, merge launch included):
+// 16-byte cp.async in fragment order 205 us, in row order 196 us, TMA 167 us.  The
+// call takes 175 us, the kernel 166 (6.45 TB/s); B=16, 16 heads, 16384-32768 tokens
+// 259 us (6.2 TB/s of 6.57).  CTAs of equal ranges (decode_sched.h) end up to 20 %
+// apart, but the memory is saturated until the last one does: ranges taken from a
+// counter gained nothing.
 //
 // Numerics.  e4m3 codes are exact in fp16; q and rho are brought to fp16 by a
 // power of two per vector (exact down to 2^-22 of the vector's largest
@@ -149,14 +152,18 @@ template <int D, bool Q8, bool RHO, int NT> struct Shape {
     static constexpr int BOXES = ROW / RB;               // boxes of a K or V tile
     static constexpr int PART = 16 * ROW;                // bytes of 16 tokens of K or V
     // 16-token parts of a tile: two, so that a warp has two independent chains of products
-    // and half the work around them (one where two stages of two would leave one CTA per SM)
+    // and half the work around them (8 heads with probes: 134 -> 121 us); one of 256-byte
+    // rows, where two stages of two would leave one CTA per SM
     static constexpr int SUBS = Q8 || D == 64 ? 2 : 1;
     static constexpr int TILE_TOKENS = 16 * SUBS;
     static constexpr int HALF = SUBS * PART;             // bytes of a K or V tile
     static constexpr int TILE_BYTES = 2 * HALF;
     static constexpr int QUAD = WARPS * TILE_TOKENS;     // tokens of one tile per warp: the schedule's step
     static constexpr int STAGES = TILE_BYTES <= 4096 ? 3 : 2;            // tiles of a warp's ring
-    // CTAs per SM that registers (128, 168 and 255 a thread) and rings leave room for
+    // CTAs per SM that registers (128, 168 and 255 a thread) and rings leave room for.
+    // Measured at d = 128, 16-token tiles (per-head cache above): 4 CTAs of 2 stages 176 us,
+    // 3 of 4 181, 4 of 3 191; 32-token tiles, 3 of 2: 176.  Two n-tiles: 3 CTAs would spill
+    // at d = 128 (125 against 120 us) and do not at d = 64 (29.0 against 29.5).
     static constexpr int CTAS = NT == 2 && D == 128 ? 2 : (NT == 1 && Q8 && D == 64 ? 4 : 3);
     static constexpr int RING_BYTES = WARPS * STAGES * TILE_BYTES;
     static constexpr int BAR_OFF = RING_BYTES > MERGE_BYTES ? RING_BYTES : MERGE_BYTES;
