@@ -27,14 +27,15 @@
  *     prints, never aborts and never falls back to another implementation.
  *   - Device-side waits are bounded.  A wait that gives up records
  *     PARALLAX_ERR_DEVICE_TIMEOUT in a per-device error word and the kernel
- *     returns; an out-of-range page id met by the paged decode records
+ *     returns; an out-of-range page id met by a paged call records
  *     PARALLAX_ERR_DEVICE_INDEX there, and a non-finite prefill output
  *     PARALLAX_ERR_DEVICE_RANGE.  Read (and clear) it with
  *     parallax_last_device_error().
  *   - Scratch.  A call that needs scratch device memory (parallax_fwd and its
  *     variants on the tensor-core path: a work counter and a block-scaled fp16
- *     copy of V; parallax_decode, parallax_softmax_decode and
- *     parallax_decode_paged: the split partials; parallax_bwd: its work
+ *     copy of V; parallax_decode, parallax_softmax_decode,
+ *     parallax_decode_paged and parallax_decode_paged_q8 / _acc: the split
+ *     partials, and for the latter two's weights the scores; parallax_bwd: its work
  *     counters and per-row statistics) takes it
  *     for that call alone from a library-owned, per-device stream-ordered
  *     memory pool

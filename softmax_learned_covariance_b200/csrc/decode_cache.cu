@@ -52,8 +52,6 @@ namespace plx {
 namespace {
 
 constexpr int WARPS = 4;
-// Tables of at most this many tokens: one CTA per item, no merge.
-constexpr int WHOLE_TOKENS = 256;
 constexpr float MNONE = -1e30f;     // reference of a row that has seen no score
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -1035,6 +1033,20 @@ cudaError_t launch_q(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, voi
     return A.kexp ? launch_d<D, true, Tout>(A, sc, mem, ctl, s) : launch_d<D, false, Tout>(A, sc, mem, ctl, s);
 }
 
+// Whether each item goes to one CTA, without cuts and (but for weights) a second launch,
+// instead of equal ranges.  By the table's tokens and the items, us with one CTA per
+// item against equal ranges (32 on 8 heads, d = 128, half to full tables or, *, 0 to full):
+//   e4m3, up to 512 tokens: 32 items of 512 10.3 / 12.4, with weights 16 12.9 / 12.2*, 2048 55 / 63;
+//   bf16, up to 256 (16 items of 512: 14.5 / 11.1*);
+//   up to 1024, from 96 items, without weights: 128 items 14.4 / 18.7, 32 items 14.4 / 12.4
+//     (with weights 96 items 18.4 / 15.7*);
+//   up to 2048, from four items per CTA: 2048 items of 2048 139 / 143, with weights 125 / 152*,
+//     bf16 194 / 220*; 512 items of 2048 52 / 49.
+bool one_cta_per_item(size_t items, size_t tokens, int ctas, bool q8, bool weights) {
+    return tokens <= (q8 ? 512u : 256u) || (tokens <= 1024 && items >= 96 && q8 && !weights) ||
+           (tokens <= 2048 && items >= (size_t)4 * ctas);
+}
+
 }  // namespace
 
 DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count) {
@@ -1045,7 +1057,8 @@ DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count) 
     const size_t cap = (size_t)A.pg.max_pages << A.pg.pshift;
     DecodeCacheScratch s{};
     const bool two = rho && A.pg.group > 4;      // as Shape::CTAS
-    s.ctas = cap <= WHOLE_TOKENS ? 0 : sm_count * (two && A.d == 128 ? 2 : (!two && q8 && A.d == 64 ? 4 : 3));
+    const int ctas = sm_count * (two && A.d == 128 ? 2 : (!two && q8 && A.d == 64 ? 4 : 3));
+    s.ctas = one_cta_per_item(items, cap, ctas, q8, A.wacc != nullptr) ? 0 : ctas;
     s.parts = up((size_t)2 * s.ctas * heads * (rho ? 2 : 1) * A.d * sizeof(float));
     s.hdr = up((size_t)2 * s.ctas * heads * sizeof(float4));
     s.cut = up((size_t)s.ctas * sizeof(int2));

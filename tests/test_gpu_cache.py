@@ -61,6 +61,12 @@ class Cache:
         self.tab = torch.from_numpy(self.table).to(DEV)
         self.tab2 = None if self.table2 is None else torch.from_numpy(self.table2).to(DEV)
 
+    def widen(self, tokens):
+        """The table with room for `tokens`; the new entries name no page."""
+        more = -(-tokens // self.ps) - self.table.shape[1]
+        self.table = np.concatenate([self.table, np.full((self.B, more), -9, np.int32)], 1)
+        self.tab = torch.from_numpy(self.table).to(DEV)
+
     def values(self):
         return [oc.values(c, e) for c, e in zip(self.codes, self.exp)] if self.q8 else self.pages
 
@@ -268,6 +274,8 @@ def test_decode(G, ps, d, with_rho, q8):
     q = bf16(rng.standard_normal((B, Hkv * G, d)))
     rho = bf16(rng.standard_normal((B, Hkv * G, d)) * 0.905) if with_rho else None
     check_decode(c, q, rho, [0, 1, 15, 16, 17, ps + 1, mp * ps])
+    c.widen(2320)                    # a table for which the work is cut over the CTAs whatever the lengths
+    check_decode(c, q, rho, [mp * ps, 33, 0, 1, 2 * ps, ps - 1, 0])
 
 
 @pytest.mark.parametrize("q8", [True, False])
@@ -296,6 +304,10 @@ def test_decode_many_sequences_and_bf16_output():
     check_decode(c, q, rho, list(sl), out_dtype=torch.bfloat16)
     check_decode(c, q, None, list(rng.integers(0, 3, 150)))
     check_decode(c, q, None, [0] * 150)
+    c.widen(2500)                    # and cut over the CTAs
+    check_decode(c, q, rho, list(sl), out_dtype=torch.bfloat16)
+    check_decode(c, q, None, list(rng.integers(0, 3, 150)))
+    check_decode(c, q, None, [0] * 150)
 
 
 def test_decode_with_heavy_and_light_blocks():
@@ -313,6 +325,9 @@ def test_decode_with_heavy_and_light_blocks():
     q, rho = bf16(rng.standard_normal((B, 4, d))), bf16(rng.standard_normal((B, 4, d)))
     check_decode(c, q, rho, [mp * ps, mp * ps - 5])
     check_decode(c, q, None, [mp * ps, mp * ps - 5])
+    c.widen(3000)
+    check_decode(c, q, rho, [mp * ps, mp * ps - 5])
+    check_decode(c, q, None, [mp * ps - 7, mp * ps])
 
 
 @pytest.mark.parametrize("scale", [(1.0, 1e-12), (1e-10, 1e-30), (1.0, 1e12), (3.0, 1e-5)])
@@ -323,8 +338,10 @@ def test_decode_of_small_and_large_values(scale):
     q, rho = bf16(rng.standard_normal((8, 8, 128)) / scale[0]), bf16(rng.standard_normal((8, 8, 128)) * 0.1 / scale[0])
     for r in (rho, None):
         check_decode(c, q, r, [1, 5, 16, 17, 33, 47, 130, 144])
-    for c, d in ((Cache(rng, 3, 1, 16, 40, 64, scale=scale), 64),):
-        check_decode(c, bf16(rng.standard_normal((3, 3, d)) / scale[0]), None, [640, 393, 7])
+    c.widen(2100)
+    check_decode(c, q, rho, [1, 5, 16, 17, 33, 47, 130, 144])
+    c = Cache(rng, 3, 1, 16, 40, 64, scale=scale)
+    check_decode(c, bf16(rng.standard_normal((3, 3, 64)) / scale[0]), None, [640, 393, 7])
 
 
 def test_decode_ignores_what_lies_behind_a_sequence():
