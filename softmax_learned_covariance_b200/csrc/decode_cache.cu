@@ -113,6 +113,11 @@ template <> __device__ __forceinline__ void store_y<__nv_bfloat16>(__nv_bfloat16
     *p = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ void store_y2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
+__device__ __forceinline__ void store_y2(__nv_bfloat16 *p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
+}
+
 constexpr int BAD = 1 << 16;     // a part's page id is out of range
 // Exponents (-128, -128) of a part that is not there: below any other, so that it
 // never sets the exponent O and M are held at.
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
     const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ rho, const signed char *__restrict__ kexp,
     const signed char *__restrict__ vexp, const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse,
-    int B, int Hq, int htiles, bool whole, PagedKV pg, Scratch ws, DeviceCtl ctl) {
+    int B, int Hq, int htiles, Split split, PagedKV pg, Scratch ws, DeviceCtl ctl) {
     using S = Shape<D, Q8, RHO, NT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023) & 1023);
@@ -208,13 +213,22 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
+    // whole items, by the CTA or by each of its warps alone: tiles first_w, first_w + step_w, ..
+    const bool whole = split != Split::RANGES, solo = split == Split::WARPS;
+    const int first_w = solo ? 0 : warp, step_w = solo ? 1 : WARPS;
+    if (threadIdx.x == 0) abort_flag = 0;
+    if (lane == 0)
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(full + 8 * i, 1);
+    fence_mbar_init();
+    __syncthreads();                         // the last of the CTA in solo mode
     // ---- this CTA's range of quads: from quad `q0` of item `it` of sequence `b`, `left` quads ----
     int b, it, q0 = 0, cta = 0, nctas = 1;
     long long left, pos = 0, total = 1;
-    if (whole) {                             // one item per CTA
-        b = blockIdx.x / per_seq;
-        it = blockIdx.x % per_seq;
-        left = quads_of(len_of(b), S::QUAD);
+    if (whole) {
+        const int x = solo ? blockIdx.x * WARPS + warp : blockIdx.x;
+        b = x / per_seq;                     // B for a warp without an item
+        it = x % per_seq;
+        left = b < B ? quads_of(len_of(b), S::QUAD) : 0;
     } else {
         // prefix sums of the sequences' quads: a run of sequences per thread, then over the threads
         const int run = (B + WARPS * 32 - 1) / (WARPS * 32);
@@ -263,17 +277,12 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
     // sequences without a token: nothing else writes their rows
     for (int e = whole ? b : (int)blockIdx.x; e < B; e += whole ? B : (int)gridDim.x) {
         if (len_of(e) > 0 || (whole && it != 0)) continue;
-        for (int i = threadIdx.x; i < Hq * D; i += WARPS * 32) store_y<Tout>(y + (size_t)e * Hq * D + i, 0.f);
+        for (int i = first_w * 32 + lane; i < Hq * D; i += step_w * 32) store_y<Tout>(y + (size_t)e * Hq * D + i, 0.f);
         if (lse != nullptr)
-            for (int i = threadIdx.x; i < Hq; i += WARPS * 32) lse[(size_t)e * Hq + i] = -INFINITY;
+            for (int i = first_w * 32 + lane; i < Hq; i += step_w * 32) lse[(size_t)e * Hq + i] = -INFINITY;
     }
     if (left == 0) return;
 
-    if (threadIdx.x == 0) abort_flag = 0;
-    if (lane == 0)
-        for (int i = 0; i < S::STAGES; ++i) mbar_init(full + 8 * i, 1);
-    fence_mbar_init();
-    __syncthreads();
     const WaitCtl wait{ctl.err, &abort_flag, ctl.wait_ns};
     int stage = 0;               // stage of this warp's next tile
     uint32_t phases = 0;         // parity each stage's barrier completes next
@@ -304,12 +313,12 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         }
         int evref = -1000;        // exponent O and M are held at (e4m3)
 
-        // This warp's tiles are warp + WARPS j.  Lane l holds the page of its 16-token part
+        // This warp's tiles are first_w + step_w j.  Lane l holds the page of its 16-token part
         // 32 n + l (a part's rows share one page: it starts on a multiple of 16 and pages
         // hold at least 16) and its two exponents, loaded 32 parts at a time.
-        const int mine = ntiles > warp ? (ntiles - warp + WARPS - 1) / WARPS : 0;
+        const int mine = ntiles > first_w ? (ntiles - first_w + step_w - 1) / step_w : 0;
         auto token_of = [&](int part) {
-            return t0 + (warp + WARPS * (part / S::SUBS)) * S::TILE_TOKENS + (part % S::SUBS) * 16;
+            return t0 + (first_w + step_w * (part / S::SUBS)) * S::TILE_TOKENS + (part % S::SUBS) * 16;
         };
         auto page_of = [&](int part) -> int {
             const int t = token_of(part);
@@ -418,6 +427,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         const int va = row_of<S::RB>(2 * t4), vb = row_of<S::RB>(2 * t4 + 1);
         const int vc = S::VB < 16 ? r / 2 : r, vsub = S::VB < 16 ? 8 * (r & 1) : 0;
         const int voff[2] = {S::HALF + chunk_at<S::RB>(va, vc) + vsub, S::HALF + chunk_at<S::RB>(vb, vc) + vsub};
+        bool gave_up = false;
         for (int j = 0; j < mine; ++j) {
             // ---- pages and exponents of the 32 parts after these, in good time ----
             constexpr int PER32 = 32 / S::SUBS;
@@ -444,6 +454,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             }
             const bool landed = mbar_wait(full + 8 * stage, (phases >> stage) & 1u, wait);
             if (!__all_sync(0xffffffffu, landed)) {
+                gave_up = true;
                 // give up: let this warp's copies land (bounded) before the CTA's memory goes
                 for (int i = j; i < min(jn + 1, mine); ++i) {
                     const int st = (stage + i - j) % S::STAGES;
@@ -668,11 +679,46 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                 }
             }
         }
+        const float oscale = Q8 ? exp2_whole(evref) : 1.f;
+        if (solo) {
+            // the item is this warp's alone: the thread that holds a head's O[d] also holds its M[d]
+            if (gave_up) return;
+#pragma unroll
+            for (int h = 0; h < S::HPT; ++h) {
+                const int head = RHO ? 4 * h + t4 : 8 * (h / 2) + 2 * t4 + h % 2, nt = RHO ? h : h / 2;
+                float l = lsum[h], ab = asum[h];
+#pragma unroll
+                for (int off = 4; off < 32; off *= 2) {
+                    l += __shfl_xor_sync(0xffffffffu, l, off);
+                    ab += __shfl_xor_sync(0xffffffffu, ab, off);
+                }
+                if (head >= nh) continue;
+                const float inv = 1.f / l, c = ab * inv, so = oscale * inv;
+                Tout *yr = y + (h0 + head) * D;
+#pragma unroll
+                for (int j = 0; j < S::JS; ++j) {
+                    const int d = Q8 || S::VB == 16 ? (S::VB / S::EL) * r + 2 * j : 64 * (j / 4) + 8 * r + 2 * (j % 4);
+                    if constexpr (RHO) {
+                        const float o0 = oacc[nt][j][0] * so, o1 = oacc[nt][j][2] * so;
+                        store_y2(yr + d, o0 - (oacc[nt][j][1] * (so * ASCALE) - o0 * c),
+                                 o1 - (oacc[nt][j][3] * (so * ASCALE) - o1 * c));
+                    } else {
+                        store_y2(yr + d, oacc[nt][j][h % 2] * so, oacc[nt][j][2 + h % 2] * so);
+                    }
+                }
+                if (r == 0) {
+                    const float l2 = mref[h] + log2f(l);
+                    if (lse != nullptr) lse[h0 + head] = l2 * LN2;
+                    if (ws.lse2 != nullptr) ws.lse2[h0 + head] = l2;
+                    if (ws.item != nullptr && h == 0 && t4 == 0) ws.item[item] = make_int2(0, 1);
+                }
+            }
+            return;
+        }
         __syncthreads();   // every warp is done with its ring: reuse it for the merge
         if (abort_flag) return;
 
         // ---- merge the warps' states per head ----
-        const float oscale = Q8 ? exp2_whole(evref) : 1.f;
         float *mg = merge + warp * S::HEADS * S::MSTRIDE;
 #pragma unroll
         for (int h = 0; h < S::HPT; ++h) {
@@ -992,16 +1038,16 @@ cudaError_t launch_t(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, voi
     ws.item = reinterpret_cast<int2 *>(take(sc.item));
     ws.lse2 = reinterpret_cast<float *>(take(sc.lse2));
     ws.zs = reinterpret_cast<float *>(take(sc.zs));
-    const bool whole = sc.ctas == 0;
-    const int grid = whole ? A.B * A.pg.Hkv * htiles : sc.ctas;
+    const bool whole = sc.split != Split::RANGES;
+    const int items = A.B * A.pg.Hkv * htiles;
+    const int grid = !whole ? sc.ctas : (sc.split == Split::WARPS ? (items + WARPS - 1) / WARPS : items);
     static std::atomic<unsigned long long> limit_set{0};
     if (cudaError_t e = ensure_smem_limit(k_decode_cache<D, Q8, RHO, NT, Tout>, S::SMEM, limit_set)) return e;
     k_decode_cache<D, Q8, RHO, NT, Tout><<<grid, WARPS * 32, S::SMEM, s>>>(
-        A.tmk, A.tmv, (const __nv_bfloat16 *)A.q, (const __nv_bfloat16 *)A.rho, A.kexp, A.vexp, A.seqlens, (Tout *)A.y, A.lse, A.B, A.Hq, htiles, whole, A.pg, ws, ctl);
+        A.tmk, A.tmv, (const __nv_bfloat16 *)A.q, (const __nv_bfloat16 *)A.rho, A.kexp, A.vexp, A.seqlens, (Tout *)A.y, A.lse, A.B, A.Hq, htiles, sc.split, A.pg, ws, ctl);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (whole && A.wacc == nullptr)) return e;
     // few items have many parts each and take a block per head, many items have two or three
-    const int items = A.B * A.pg.Hkv * htiles;
     const int hpb = items >= 128 ? S::HEADS : 1;
     const int combine = whole ? 0 : (hpb == 1 ? items * S::HEADS : grid);
     const int acc_chunks = A.wacc ? (Tcap + ACC_TOKENS - 1) / ACC_TOKENS : 0;
@@ -1033,18 +1079,22 @@ cudaError_t launch_q(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, voi
     return A.kexp ? launch_d<D, true, Tout>(A, sc, mem, ctl, s) : launch_d<D, false, Tout>(A, sc, mem, ctl, s);
 }
 
-// Whether each item goes to one CTA, without cuts and (but for weights) a second launch,
-// instead of equal ranges.  By the table's tokens and the items, us with one CTA per
-// item against equal ranges (32 on 8 heads, d = 128, half to full tables or, *, 0 to full):
-//   e4m3, up to 512 tokens: 32 items of 512 10.3 / 12.4, with weights 16 12.9 / 12.2*, 2048 55 / 63;
-//   bf16, up to 256 (16 items of 512: 14.5 / 11.1*);
-//   up to 1024, from 96 items, without weights: 128 items 14.4 / 18.7, 32 items 14.4 / 12.4
-//     (with weights 96 items 18.4 / 15.7*);
-//   up to 2048, from four items per CTA: 2048 items of 2048 139 / 143, with weights 125 / 152*,
-//     bf16 194 / 220*; 512 items of 2048 52 / 49.
-bool one_cta_per_item(size_t items, size_t tokens, int ctas, bool q8, bool weights) {
-    return tokens <= (q8 ? 512u : 256u) || (tokens <= 1024 && items >= 96 && q8 && !weights) ||
-           (tokens <= 2048 && items >= (size_t)4 * ctas);
+// How the work is split, by the table's tokens, the items and the CTAs that are resident.
+// us measured, 32 on 8 heads, d = 128, e4m3, half to full tables (*: 0 to full).
+//   A warp per item (no merge at all, four times the items under way): 512 items of 256
+//   tokens 14.4 against 16.5 with a CTA each, 1024 of 512 28.8 / 34.5, 4096 of 128 33 / 61,
+//   8192 of 64 41 / 105; but 512 of 512 22.6 / 21.5, 128 of 128 10.3 / 8.3, and with weights
+//   in bf16 512 of 256 22.6 / 18.6*, 1024 of 512 45 / 58*, 4096 of 128 49 / 72*.
+//   A CTA per item (no cuts and, but for weights, no second launch) against equal ranges:
+//   32 items of 512 10.3 / 12.4, with weights 16 12.9 / 12.2*, bf16 14.5 / 11.1*; without
+//   weights 128 items of 1024 14.4 / 18.7, 32 14.4 / 12.4, with weights 96 18.4 / 15.7*;
+//   2048 items of 2048 139 / 143, with weights 125 / 152*, bf16 194 / 220*; 512 52 / 49.
+Split split_of(size_t items, size_t tokens, size_t ctas, bool q8, bool weights) {
+    if ((tokens <= 256 && items >= (q8 ? 1 : 2) * ctas) || (tokens <= 512 && items >= 2 * ctas)) return Split::WARPS;
+    if (tokens <= (q8 ? 512u : 256u) || (tokens <= 1024 && items >= 96 && q8 && !weights) ||
+        (tokens <= 2048 && items >= 4 * ctas))
+        return Split::CTAS;
+    return Split::RANGES;
 }
 
 }  // namespace
@@ -1058,7 +1108,8 @@ DecodeCacheScratch decode_cache_scratch(const DecodeCacheArgs &A, int sm_count) 
     DecodeCacheScratch s{};
     const bool two = rho && A.pg.group > 4;      // as Shape::CTAS
     const int ctas = sm_count * (two && A.d == 128 ? 2 : (!two && q8 && A.d == 64 ? 4 : 3));
-    s.ctas = one_cta_per_item(items, cap, ctas, q8, A.wacc != nullptr) ? 0 : ctas;
+    s.split = split_of(items, cap, ctas, q8, A.wacc != nullptr);
+    s.ctas = s.split == Split::RANGES ? ctas : 0;
     s.parts = up((size_t)2 * s.ctas * heads * (rho ? 2 : 1) * A.d * sizeof(float));
     s.hdr = up((size_t)2 * s.ctas * heads * sizeof(float4));
     s.cut = up((size_t)s.ctas * sizeof(int2));

@@ -86,8 +86,10 @@ inline int decode_cache_box(int d, bool bf16) { return bf16 ? 64 : d; }
 // How a call is cut (decode_sched.h) and its scratch in bytes, each part a multiple
 // of 256: parts of the cut items, their headers, which items are cut, and, with
 // weights, the items' parts, the logs of their sums and the scores.
+enum class Split { RANGES, CTAS, WARPS };     // equal ranges per CTA, or whole items, one per CTA or warp
 struct DecodeCacheScratch {
-    int ctas;      // 0: one CTA per item
+    Split split;
+    int ctas;      // of equal ranges
     size_t parts, hdr, cut, item, lse2, zs;
     size_t bytes() const { return parts + hdr + cut + item + lse2 + zs; }
 };

@@ -310,6 +310,31 @@ def test_decode_many_sequences_and_bf16_output():
     check_decode(c, q, None, [0] * 150)
 
 
+@pytest.mark.parametrize("q8", [True, False])
+@pytest.mark.parametrize("with_rho", [True, False])
+@pytest.mark.parametrize("G", [3, 6])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_many_short_sequences(d, G, with_rho, q8):
+    """So many short items that each warp has its own."""
+    rng = np.random.default_rng(17 + G)
+    B, Hkv = 310, 4
+    c = Cache(rng, B, Hkv, 16, 8, d, q8)
+    q = bf16(rng.standard_normal((B, Hkv * G, d)))
+    rho = bf16(rng.standard_normal((B, Hkv * G, d)) * 0.905) if with_rho else None
+    sl = rng.integers(0, 129, B)
+    sl[:3] = sl[-2:] = 0
+    check_decode(c, q, rho, list(sl))
+    c.tab[7, 2:] = c.n + 1                                     # bad pages in one item only
+    sld = torch.from_numpy(np.full(B, 128, np.int32)).to(DEV)
+    w = torch.zeros((B, Hkv, 128), device=DEV)
+    args = (q.to(DEV), None if rho is None else rho.to(DEV), c.kp, c.vp)
+    y, lse = plx.parallax_decode_paged_q8(*args, c.ke, c.ve, c.tab, sld, wacc=w) if q8 else \
+        plx.parallax_decode_paged_acc(*args, c.tab, sld, w)
+    assert plx.parallax_last_device_error() == 8
+    assert torch.isfinite(y).all() and torch.isfinite(lse).all()
+    assert np.allclose(w.sum(2).cpu().numpy(), G, rtol=1e-4)
+
+
 def test_decode_with_heavy_and_light_blocks():
     """Scores that rise late in the cache, V blocks whose exponents differ by far, a zero V block under the peak."""
     rng = np.random.default_rng(10)
@@ -692,20 +717,29 @@ def test_offsets_past_32_bits():
     no_error()
 
 
-def test_forced_wait_timeout_is_reported_and_recoverable(monkeypatch):
+@pytest.mark.parametrize("split", ["ranges", "ctas", "warps"])
+def test_forced_wait_timeout_is_reported_and_recoverable(split, monkeypatch):
     """Test hook: no warp copies its first tile, so its bounded wait expires; the next call is right again."""
     rng = np.random.default_rng(34)
-    c = Cache(rng, 2, 2, 16, 30, 128)
-    q = bf16(rng.standard_normal((2, 4, 128))).to(DEV)
-    sl = torch.tensor([480, 100], dtype=torch.int32, device=DEV)
-    ok, _ = plx.parallax_decode_paged_q8(q, q, c.kp, c.vp, c.ke, c.ve, c.tab, sl)
+    B, mp = (300, 2) if split == "warps" else (2, 30)
+    c = Cache(rng, B, 2, 16, mp, 128)
+    if split == "ranges":
+        c.widen(2400)
+    q = bf16(rng.standard_normal((B, 4, 128))).to(DEV)
+    sl = torch.tensor([mp * 16, 20] * (B // 2), dtype=torch.int32, device=DEV)
+
+    def call():
+        w = torch.zeros((B, 2, c.table.shape[1] * 16), device=DEV)
+        return plx.parallax_decode_paged_q8(q, q, c.kp, c.vp, c.ke, c.ve, c.tab, sl, wacc=w)[0]
+
+    ok = call()
     no_error()
     monkeypatch.setenv("PARALLAX_DEBUG_FLAGS", "2")
     monkeypatch.setenv("PARALLAX_WAIT_TIMEOUT_MS", "50")
-    plx.parallax_decode_paged_q8(q, q, c.kp, c.vp, c.ke, c.ve, c.tab, sl)
+    call()
     assert plx.parallax_last_device_error() == 7
     monkeypatch.delenv("PARALLAX_DEBUG_FLAGS")
     monkeypatch.delenv("PARALLAX_WAIT_TIMEOUT_MS")
-    y, _ = plx.parallax_decode_paged_q8(q, q, c.kp, c.vp, c.ke, c.ve, c.tab, sl)
+    y = call()
     no_error()
     assert torch.equal(y, ok)
