@@ -320,9 +320,11 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         auto token_of = [&](int part) {
             return t0 + (first_w + step_w * (part / S::SUBS)) * S::TILE_TOKENS + (part % S::SUBS) * 16;
         };
+        // (read up to the table's end: the entries past t1 are not followed, and their load does not wait
+        // for the length)
         auto page_of = [&](int part) -> int {
             const int t = token_of(part);
-            return t < t1 ? pg.table[(size_t)b * pg.max_pages + (t >> pg.pshift)] : 0;
+            return t < Tcap ? pg.table[(size_t)b * pg.max_pages + (t >> pg.pshift)] : 0;
         };
         // exponents of K (low byte) and V (next byte), and BAD for a page id out of range
         auto info_of = [&](int part, int id) -> int {
@@ -336,7 +338,21 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             const size_t at = ((size_t)id * pg.Hkv + kvh) * (ps / KV_BLOCK) + (t & pmask) / KV_BLOCK;
             return (kexp[at] & 0xff) | (vexp[at] & 0xff) << 8;
         };
-        int ids = page_of(lane), ids_next = 0, info = info_of(lane, ids), info_next = 0;
+        int ids = page_of(lane), ids_next = 0;
+        // the vectors, column n = r of n-tile nt, as they are: loaded before anything waits for the pages
+        uint2 qw[NT][S::KSTEPS];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int head = RHO ? nt * 4 + r / 2 : nt * 8 + r;
+            const bool live = head < nh;
+            const __nv_bfloat16 *src = (RHO && (r & 1) ? rho : q) + (h0 + (live ? head : 0)) * D;
+#pragma unroll
+            for (int s = 0; s < S::KSTEPS; ++s) {
+                const int d0 = Q8 ? 64 * (s / 4) + 16 * t4 + 4 * (s % 4) : 32 * (s / 2) + 8 * t4 + 4 * (s % 2);
+                qw[nt][s] = live ? *reinterpret_cast<const uint2 *>(src + d0) : make_uint2(0u, 0u);
+            }
+        }
+        int info = info_of(lane, ids), info_next = 0;
 
         uint8_t *ring = smem + warp * S::STAGES * S::TILE_BYTES;
         // Loads tile j into stage st; lane l holds the page of part 32 n + l in `pages`.
@@ -375,15 +391,10 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
         float zfac[S::HPT], afac[S::HPT];    // of the heads whose state this thread holds
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int head = RHO ? nt * 4 + r / 2 : nt * 8 + r;
-            const bool live = head < nh;
-            const __nv_bfloat16 *src = (RHO && (r & 1) ? rho : q) + (h0 + (live ? head : 0)) * D;
-            uint2 w[S::KSTEPS];
+            const uint2 *w = qw[nt];
             uint32_t big = 0;
 #pragma unroll
             for (int s = 0; s < S::KSTEPS; ++s) {
-                const int d0 = Q8 ? 64 * (s / 4) + 16 * t4 + 4 * (s % 4) : 32 * (s / 2) + 8 * t4 + 4 * (s % 2);
-                w[s] = live ? *reinterpret_cast<const uint2 *>(src + d0) : make_uint2(0u, 0u);
                 big = max(big, max(max(w[s].x & 0x7fffu, w[s].x >> 16 & 0x7fffu), max(w[s].y & 0x7fffu, w[s].y >> 16 & 0x7fffu)));
             }
             float inv = 1.f;

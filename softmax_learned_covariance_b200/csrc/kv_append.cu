@@ -68,9 +68,9 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_append(KvAppendArgs A, unsign
         if (over) atomicExch(err, PARALLAX_ERR_DEVICE_INDEX);
         if (A.new_seqlens) A.new_seqlens[b] = start + n;
     }
+    if (n == 0 || blk > (start + n - 1) / KV_BLOCK - start / KV_BLOCK) return;   // no new row
     const int p0 = (start / KV_BLOCK + blk) * KV_BLOCK;      // the block's first position
     const int lo = max(start - p0, 0), hi = min(start + n - p0, KV_BLOCK);   // its new rows
-    if (n == 0 || hi <= lo) return;
     const int id = A.pg.table[(size_t)b * A.pg.max_pages + (p0 >> A.pg.pshift)];
     if ((unsigned)id >= (unsigned)A.pg.num_pages) {
         if (lane == 0) atomicExch(err, PARALLAX_ERR_DEVICE_INDEX);
