@@ -374,35 +374,24 @@ def parallax_decode_paged_q8(q, rho, kpages, vpages, kexp, vexp, block_table, se
     [B, Hkv, max_pages * page_size], to which the attention weight of each cached token, summed over
     the query heads of its KV head, is added.
     """
-    torch = _torch()
-    if kpages.dtype != torch.float8_e4m3fn:
-        raise TypeError("kpages must be float8_e4m3fn")
-    return _decode_cache("parallax_decode_paged_q8", torch, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens,
-                         wacc, out_dtype, y, lse, stream, want_lse)
+    return _decode_cache("parallax_decode_paged_q8", stream, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens,
+                         wacc, y, lse, out_dtype, want_lse, True)
 
 
 def parallax_decode_paged_acc(q, rho, kpages, vpages, block_table, seqlens, wacc, out_dtype=None, y=None, lse=None,
                               stream=None, want_lse: bool = True):
     """parallax_decode_paged_q8 over a bf16 paged cache; wacc is required."""
-    torch = _torch()
-    if kpages.dtype != torch.bfloat16:
-        raise TypeError("kpages must be bfloat16")
     if wacc is None:
         raise ValueError("wacc is required; without it use parallax_decode_paged")
-    return _decode_cache("parallax_decode_paged_acc", torch, q, rho, kpages, vpages, None, None, block_table, seqlens,
-                         wacc, out_dtype, y, lse, stream, want_lse)
+    return _decode_cache("parallax_decode_paged_acc", stream, q, rho, kpages, vpages, None, None, block_table, seqlens,
+                         wacc, y, lse, out_dtype, want_lse, False)
 
 
-def _decode_cache(name, torch, q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, out_dtype, y, lse,
-                  stream, want_lse):
-    if out_dtype is not None and out_dtype != torch.float32 and out_dtype != torch.bfloat16:
-        raise TypeError(f"unsupported dtype {out_dtype}")
-    args = (q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, y, lse, out_dtype == torch.bfloat16,
-            bool(want_lse))
+def _decode_cache(name, stream, *args):
     if stream is None:
         r = _native().decode(*args)
     else:
-        with _on(kpages, stream):
+        with _on(args[2], stream):
             r = _native().decode(*args)
     if type(r) is int:
         _check(r, name)

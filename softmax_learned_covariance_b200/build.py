@@ -67,7 +67,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{i}" for i in inc),
-           BINDING_SRC, "-o", tmp, f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           BINDING_SRC, "-o", tmp, f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
            f"-Wl,-rpath,{libs}"]
     if verbose:
         print(" ".join(cmd), flush=True)

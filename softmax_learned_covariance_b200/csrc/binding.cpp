@@ -12,8 +12,10 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -104,8 +106,9 @@ Cache cache(PyObject *k, PyObject *v, PyObject *kexp, PyObject *vexp, PyObject *
 
 void *stream_of(const at::Device &dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
+// An uninitialised tensor from torch's allocator, without the dispatcher's 0.5 us.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
 
 PyObject *wrap(const at::Tensor &t) {
@@ -144,10 +147,19 @@ long long whole(PyObject *o) {
     return x;
 }
 
-// (q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, y, lse, bf16_out, want_lse) -> (y, lse)
+// (q, rho, kpages, vpages, kexp, vexp, block_table, seqlens, wacc, y, lse, out_dtype, want_lse, q8) -> (y, lse)
 PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (!count(n, 13)) return nullptr;
+    if (!count(n, 14)) return nullptr;
+    at::ScalarType out_type = at::kFloat;
+    if (a[11] != Py_None) {
+        if (!THPDtype_Check(a[11])) bad_type("out_dtype", "a dtype");
+        out_type = reinterpret_cast<THPDtype *>(a[11])->scalar_type;
+        TORCH_CHECK_TYPE(out_type == at::kFloat || out_type == at::kBFloat16, "unsupported dtype ", out_type);
+    }
+    const bool want_q8 = a[13] == Py_True;
+    TORCH_CHECK_TYPE(tensor(a[2], "kpages").scalar_type() == (want_q8 ? at::kFloat8_e4m3fn : at::kBFloat16),
+                     "kpages must be ", want_q8 ? "float8_e4m3fn" : "bfloat16");
     const Cache c = cache(a[2], a[3], a[4], a[5], a[6], a[7]);
     const at::Tensor q = tensor(a[0], "q"), rho = tensor(a[1], "rho", true), wacc = tensor(a[8], "wacc", true);
     at::Tensor y = tensor(a[9], "y", true), lse = tensor(a[10], "lse", true);
@@ -162,11 +174,11 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
         TORCH_CHECK_TYPE(y.scalar_type() == at::kFloat || y.scalar_type() == at::kBFloat16, "unsupported dtype of y");
         is(y, "y", y.scalar_type(), shape, c.dev);
     } else {
-        y = fresh(shape, a[11] == Py_True ? at::kBFloat16 : at::kFloat, c.dev);
+        y = fresh(shape, out_type, c.dev);
     }
     if (lse.defined())
         is(lse, "lse", at::kFloat, {c.B, Hq}, c.dev);
-    else if (a[12] == Py_True)
+    else if (PyObject_IsTrue(a[12]) == 1)
         lse = fresh({c.B, Hq}, at::kFloat, c.dev);
     const int out = y.scalar_type() == at::kFloat ? PARALLAX_F32 : PARALLAX_BF16;
     const int B = (int)c.B, hq = small(Hq, "Hq"), hkv = (int)c.Hkv, ps = small(c.ps, "page_size"), d = small(c.d, "d");
