@@ -321,7 +321,8 @@ PARALLAX_API int parallax_decode_noalloc(const void *q, const void *rho, const v
  *   wacc : NULL, or fp32 [B, Hkv, max_pages * page_size]: for t < seqlens[b],
  *          wacc[b, h, t] += sum over the KV head's query heads of the softmax
  *          weight s_t.  Other entries are not touched.  16-byte aligned.
- *   Everything else as parallax_decode_paged.  |k.rho| < 65504.
+ *   Everything else as parallax_decode_paged, but that table entries past a
+ *   sequence's last page may be read (they are not followed).  |k.rho| < 65504.
  * Results do not depend on the schedule (no atomics).  Scratch: split partials,
  * and with wacc 4 bytes per (sequence, token slot of the table, query head
  * rounded up to a multiple of 4, of 8 without rho or above 4 per KV head).
