@@ -1,7 +1,8 @@
 // binding.cpp -- the paged-cache calls of the Python binding in native code.
 //
 // A decode step of one short sequence takes the GPU a few microseconds; checking
-// a dozen tensors and allocating two outputs from Python took 16.  These functions
+// a dozen tensors and allocating two outputs from Python took 16 (26 before that was
+// made as lean as it gets); a whole call takes 6 to 7 with these functions, which
 // do the same -- check, allocate on the tensors' device and its current stream,
 // call the C ABI -- and nothing else; the library's entry points are handed over
 // by address (bind), so there is one loaded library and no second path.
