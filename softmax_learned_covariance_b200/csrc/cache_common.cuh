@@ -26,11 +26,6 @@ __device__ __forceinline__ uint4 ldg_nc16(const void *p) {
                  : "l"(p));
     return r;
 }
-__device__ __forceinline__ uint2 ldg_nc8(const void *p) {
-    uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
 
 // 4 packed e4m3 -> 2 packed fp16x2 (exact)
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t &lo, uint32_t &hi) {

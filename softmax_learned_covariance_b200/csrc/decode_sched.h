@@ -20,15 +20,10 @@
 
 namespace plx {
 
-constexpr int MIN_QUADS = 1;    // of a range, while there are CTAs to spare
-
 PLX_HD int quads_of(int tokens, int quad) { return (tokens + quad - 1) / quad; }
 
-// CTAs that take part, of `ctas`, for `total` quads
-PLX_HD int sched_ctas(long long total, int ctas) {
-    const long long n = (total + MIN_QUADS - 1) / MIN_QUADS;
-    return n < ctas ? (int)n : ctas;
-}
+// CTAs that take part, of `ctas`, for `total` quads: a quad each at least
+PLX_HD int sched_ctas(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
 // a / b, in 32 bits where they suffice (a 64-bit division takes the GPU some hundred cycles)
 PLX_HD long long sched_div(long long a, long long b) {
     return a <= 0x7fffffff && b <= 0x7fffffff ? (long long)((unsigned)a / (unsigned)b) : a / b;
