@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
     };
     __shared__ __align__(16) uint32_t hist[3][BINS];
     __shared__ uint32_t wsum[32];
-    __shared__ uint32_t found[2], mine[2];             // a digit and the keys above it; this CTA's counts
+    __shared__ uint32_t found[3], mine[2];             // a digit, the keys above it and with it; this CTA's counts
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, rank = CLUSTER ? (int)(blockIdx.x % (unsigned)cluster_size) : 0;
     const unsigned bk = blockIdx.x / (unsigned)cluster_size;
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
                         uint32_t *to = CLUSTER ? cluster.map_shared_rank(found, q) : found;
                         to[0] = (uint32_t)(top + i);
                         to[1] = before;
+                        to[2] = hist[pass][top + i];
                     }
                 }
             }
@@ -183,6 +184,13 @@ __global__ void __launch_bounds__(SEL_THREADS, CLUSTER ? 2 : 4) k_evict_select(K
             prefix |= found[0] << shift;
             mask |= digit << shift;
             left -= found[1];
+            if (found[2] == left) {
+                // every key with this prefix is wanted (after two digits nearly always: the
+                // one key there): all that are larger than the largest key below it
+                prefix -= 1u;
+                left = 0;
+                break;
+            }
         }
         ties = left;                                   // this many of the tokens whose key is `prefix`, in order
     }
