@@ -16,7 +16,7 @@
 // destination block takes the largest exponent of its rows' source blocks and the
 // rows of smaller ones are moved to it (exact until subnormal).
 //
-// Measured: 64 sequences of 3000-4096, 8 heads, 2048 kept, e4m3: 109 us a call; the
+// Measured: 64 sequences of 3000-4096, 8 heads, 2048 kept, e4m3: 108 us a call; the
 // move 86 (0.55 GB read and written, 6.3 TB/s of 6.57), the selection 18, bound by
 // instruction issue and barriers.  One sequence of 32768, 8 heads, 4096 kept, bf16:
 // 20 us, of them 12.5 the selection (41 with one CTA per head), latency.
