@@ -322,7 +322,10 @@ PARALLAX_API int parallax_decode_noalloc(const void *q, const void *rho, const v
  *          wacc[b, h, t] += sum over the KV head's query heads of the softmax
  *          weight s_t.  Other entries are not touched.  16-byte aligned.
  *   Everything else as parallax_decode_paged, but that table entries past a
- *   sequence's last page may be read (they are not followed).  |k.rho| < 65504.
+ *   sequence's last page may be read (they are not followed).
+ * The weights of o and m are carried in two 16-bit parts: what a token contributes is
+ * good to 2^-21 of it, or to 2^-35 of the largest contribution of its head where that
+ * is more (bf16 cache: 2^-16 of it); the other sums are fp32.
  * Results do not depend on the schedule (no atomics).  Scratch: split partials,
  * and with wacc 4 bytes per (sequence, token slot of the table, query head
  * rounded up to a multiple of 4, of 8 without rho or above 4 per KV head).

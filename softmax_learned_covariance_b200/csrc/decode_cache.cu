@@ -35,11 +35,18 @@
 //
 // Numerics.  e4m3 codes are exact in fp16; q and rho are brought to fp16 by a
 // power of two per vector (exact down to 2^-22 of the vector's largest
-// element); the block exponents multiply z and a in fp32, and V's enters its
-// weight relative to the warp's largest so far.  The weights p and p a are
-// carried as two 16-bit parts (fp16 hi + lo, or bf16 hi + lo for a bf16 cache,
-// whose V then needs no conversion), 2^-17 or better, so their rounding stays
-// far below the cache's own; l and abar sum the fp32 weights.
+// element); the block exponents multiply z and a in fp32.  The weights of O and M
+// are carried as two 16-bit parts.  For a bf16 cache, whose V needs no conversion,
+// these are bf16: 2^-16 of any weight.  For an e4m3 cache they are fp16, 2^-21 with
+// a smallest step of 2^-24, so what they are held against decides what is lost: per
+// head, O's weights p 2^ve (ve: V's block exponent) against the largest so far, and
+// M's, p |a| 2^ve, against their own; the largest is 2^10 to 2^15 in fp16.  What a
+// token contributes is then off by 2^-35 of the largest contribution at most, which
+// the fp32 sums lose as well.  (Held against the largest weight and the largest
+// exponent, wherever each was met, a large V or a without weight cost every other
+// token its bits.  The two references cost at most 1 % of the cases above,
+// 4 % where two n-tiles meet a new item every few tiles.)  l and abar sum the fp32
+// weights.
 #include <math.h>
 
 #include <type_traits>
@@ -55,15 +62,23 @@ constexpr int WARPS = 4;
 constexpr float MNONE = -1e30f;     // reference of a row that has seen no score
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-// A row's reference moves when a score exceeds it by 2^HEADROOM: p <= 2^4, and
-// p a is carried as p (a / 2^4), so |a| up to fp16's range stays finite.
-constexpr float HEADROOM = 4.f;
-constexpr float ASCALE = 16.f;
+// A head's references move when a weight exceeds one by 2^4 (HEADROOM); fp16 weights of
+// O and M are 2^WSHIFT at their reference, so 2^15 at most.
+constexpr float HEADROOM = 16.f;
+constexpr int WSHIFT = 11;
 
 __device__ __forceinline__ float fex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// log2 of a power of two
+__device__ __forceinline__ int whole_log2(float x) { return (__float_as_int(x) >> 23) - 127; }
+// v 2^e for e in [-250, 250]
+__device__ __forceinline__ float scaled(float v, int e) {
+    const int half = e >> 1;
+    return v * exp2_whole(half) * exp2_whole(e - half);
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -311,7 +326,14 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             mref[i] = MNONE;
             lsum[i] = asum[i] = 0.f;
         }
-        int evref = -1000;        // exponent O and M are held at (e4m3)
+        // O is held at 2^(mref + oexp), M at that over mratio, both times 2^WSHIFT (e4m3)
+        int oexp[S::HPT];
+        float mratio[S::HPT];
+#pragma unroll
+        for (int i = 0; i < S::HPT; ++i) {
+            oexp[i] = -400;       // below any that a tile sets
+            mratio[i] = 1.f;
+        }
 
         // This warp's tiles are first_w + step_w j.  Lane l holds the page of its 16-token part
         // 32 n + l (a part's rows share one page: it starts on a multiple of 16 and pages
@@ -388,7 +410,7 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             if (j < mine) issue(j, (stage + j) % S::STAGES, ids);
         // ---- the vectors (the first tiles are on their way): column n = r of n-tile nt; 4 elements per MMA step ----
         uint32_t qf[NT][S::KSTEPS][2];
-        float zfac[S::HPT], afac[S::HPT];    // of the heads whose state this thread holds
+        float zfac[S::HPT], afac[S::HPT] = {};    // of the heads whose state this thread holds
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const uint2 *w = qw[nt];
@@ -544,106 +566,129 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             // ---- weights ----
             constexpr int ROWS = 2 * S::SUBS;     // a thread's tokens: row x is 16 (x / 2) + (x odd ? tok1 : tok0)
             auto tok = [&](int x) { return 16 * (x >> 1) + ((x & 1) ? tok1 : tok0); };
-            float f[S::SUBS][S::HPT], dz[S::HPT][ROWS];       // score = sc * f; dz: against the reference
-            float kscale[S::SUBS];
-            bool up = false;
+            float f[S::SUBS][S::HPT], fa[S::SUBS][S::HPT];       // z = sc * f, a = sc * fa
 #pragma unroll
             for (int u = 0; u < S::SUBS; ++u) {
-                up |= Q8 && ve[u] > evref;
-                kscale[u] = Q8 ? exp2_whole(ke[u]) : 1.f;
-            }
+                const float kscale = Q8 ? exp2_whole(ke[u]) : 1.f;
 #pragma unroll
-            for (int h = 0; h < S::HPT; ++h) {
-                const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
-                float top = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < ROWS; ++x) {
-                    const int u = x >> 1;
-                    f[u][h] = Q8 ? fminf(zfac[h] * kscale[u], 3e38f) : zfac[h];     // finite: a score of 0 stays 0
-                    dz[h][x] = fmaf(sc[u][nt][2 * (x & 1) + e], f[u][h], -mref[h]);
-                    if (ragged && tok(x) >= nvalid) dz[h][x] = -INFINITY;
-                    top = fmaxf(top, dz[h][x]);
+                for (int h = 0; h < S::HPT; ++h) {
+                    f[u][h] = Q8 ? fminf(zfac[h] * kscale, 3e38f) : zfac[h];         // finite: a score of 0 stays 0
+                    fa[u][h] = Q8 ? fminf(afac[h] * kscale, 3e38f) : afac[h];
                 }
-                up |= top > HEADROOM;
             }
+            auto score = [&](int h, int x) { return sc[x >> 1][RHO ? h : h / 2][2 * (x & 1) + (RHO ? 0 : h % 2)]; };
+            auto masked = [&](int x) { return ragged && tok(x) >= nvalid; };
+            auto weight = [&](int h, int x) {
+                const float dz = fmaf(score(h, x), f[x >> 1][h], -mref[h]);
+                return fex2(masked(x) ? -INFINITY : dz);
+            };
+            auto probe = [&](int h, int x) { return sc[x >> 1][h][2 * (x & 1) + 1] * fa[x >> 1][h]; };
+            // weights: p against mref, and those of O and M as they are held (masked tokens have p = 0
+            // and, their K rows being zero, a = 0); whether one has outgrown its reference (NaN does not)
+            float p[S::HPT][ROWS], wo[S::HPT][ROWS], wm[S::HPT][ROWS];
+            auto weigh = [&] {
+                bool up = false;
+#pragma unroll
+                for (int h = 0; h < S::HPT; ++h) {
+                    float top = 0.f, topw = 0.f;
+#pragma unroll
+                    for (int x = 0; x < ROWS; ++x) {
+                        p[h][x] = weight(h, x);
+                        top = fmaxf(top, p[h][x]);
+                        wo[h][x] = Q8 ? p[h][x] * exp2_whole(min(ve[x >> 1] - oexp[h] + WSHIFT, 126)) : p[h][x];
+                        topw = fmaxf(topw, wo[h][x]);
+                        if constexpr (RHO) {
+                            wm[h][x] = wo[h][x] * probe(h, x);
+                            if constexpr (Q8) wm[h][x] *= mratio[h];
+                            topw = fmaxf(topw, fabsf(wm[h][x]));
+                        }
+                    }
+                    up |= top > HEADROOM;
+                    if constexpr (Q8) up |= topw > HEADROOM * (1 << WSHIFT);
+                }
+                return up;
+            };
             if (ws.zs != nullptr) {
                 float *dst = ws.zs + ((size_t)item * Tcap + tile) * S::HEADS;
 #pragma unroll
                 for (int h = 0; h < S::HPT; ++h) {
-                    const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
                     const int head = RHO ? 4 * h + t4 : 8 * (h / 2) + 2 * t4 + h % 2;
 #pragma unroll
                     for (int x = 0; x < ROWS; ++x)
-                        if (tok(x) < nvalid) dst[tok(x) * S::HEADS + head] = sc[x >> 1][nt][2 * (x & 1) + e] * f[x >> 1][h];
+                        if (tok(x) < nvalid) dst[tok(x) * S::HEADS + head] = score(h, x) * f[x >> 1][h];
                 }
             }
-            if (__any_sync(0xffffffffu, up)) {
-                int evnew = evref;
-#pragma unroll
-                for (int u = 0; u < S::SUBS; ++u) evnew = Q8 ? max(evnew, ve[u]) : evnew;
-                const float vshift = Q8 ? fex2((float)(evref - evnew)) : 1.f;
-                evref = evnew;
+            // (a warp's first tile always sets the references: a short call does not wait for the
+            // instructions of a first try, 12.5 against 14.3 us for one tile per warp)
+            if (j == 0 || __any_sync(0xffffffffu, weigh())) {
 #pragma unroll
                 for (int h = 0; h < S::HPT; ++h) {
                     const int nt = RHO ? h : h / 2, e = RHO ? 0 : h % 2;
-                    float mx = -INFINITY;
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int x = 0; x < ROWS; ++x) {
-                        dz[h][x] = sc[x >> 1][nt][2 * (x & 1) + e] * f[x >> 1][h];
-                        if (ragged && tok(x) >= nvalid) dz[h][x] = -INFINITY;
-                        mx = fmaxf(mx, dz[h][x]);
-                    }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float mnew = fmaxf(mref[h], mx);
-                    const float alpha = fex2(mref[h] - mnew);
+                    for (int x = 0; x < ROWS; ++x) top = fmaxf(top, masked(x) ? -INFINITY : score(h, x) * f[x >> 1][h]);
+#pragma unroll
+                    for (int off = 4; off < 32; off *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    const float mnew = fmaxf(mref[h], top), down = mref[h] - mnew;
+                    const float alpha = fex2(down);
                     mref[h] = mnew;
-#pragma unroll
-                    for (int x = 0; x < ROWS; ++x) dz[h][x] -= mnew;
                     lsum[h] *= alpha;
                     asum[h] *= alpha;
-                    const float beta = alpha * vshift;
+                    float bo = alpha, bm = alpha;                  // what O and M held so far becomes
+                    if constexpr (Q8) {
+                        // The whole exponents above the tile's largest p 2^ve and p |a| 2^ve: both maxima at
+                        // once, in the upper halves of their floats (one that underflows is below any that counts)
+                        float o = 0.f, m = 0.f;
+#pragma unroll
+                        for (int x = 0; x < ROWS; ++x) {
+                            const float w = weight(h, x) * exp2_whole(ve[x >> 1]);
+                            o = fmaxf(o, w);
+                            if constexpr (RHO) m = fmaxf(m, w * fabsf(probe(h, x)));
+                        }
+                        uint32_t both = __byte_perm(__float_as_uint(o), __float_as_uint(m), 0x7632);
+#pragma unroll
+                        for (int off = 4; off < 32; off *= 2) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, off));
+                        const int fell = __float2int_rd(fmaxf(down, -1e3f));     // (down: a reference never creeps up)
+                        const int eo = max((int)(both >> 7 & 255) - 126, oexp[h] + fell);
+                        bo = fex2(down + (float)(oexp[h] - eo));
+                        if constexpr (RHO) {
+                            const int held = oexp[h] - whole_log2(mratio[h]);
+                            const int em = min(max(max((int)(both >> 23) - 126, held + fell), eo - 30), eo + 126);
+                            bm = fex2(down + (float)(held - em));
+                            mratio[h] = exp2_whole(eo - em);
+                        }
+                        oexp[h] = eo;
+                    }
 #pragma unroll
                     for (int i = 0; i < S::JS; ++i) {
                         if constexpr (RHO) {
-                            oacc[nt][i][0] *= beta;
-                            oacc[nt][i][1] *= beta;
-                            oacc[nt][i][2] *= beta;
-                            oacc[nt][i][3] *= beta;
+                            oacc[nt][i][0] *= bo;
+                            oacc[nt][i][1] *= bm;
+                            oacc[nt][i][2] *= bo;
+                            oacc[nt][i][3] *= bm;
                         } else {
-                            oacc[nt][i][e] *= beta;
-                            oacc[nt][i][2 + e] *= beta;
+                            oacc[nt][i][e] *= bo;
+                            oacc[nt][i][2 + e] *= bo;
                         }
                     }
                 }
+                weigh();
             }
             uint32_t bh[NT][ROWS], bl[NT][ROWS];    // weights as the value product's operand: hi, lo parts
 #pragma unroll
             for (int x = 0; x < ROWS; ++x) {
-                const int u = x >> 1;
-                const float vfac = Q8 ? fex2((float)(ve[u] - evref)) : 1.f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float w0, w1;
-                    if constexpr (RHO) {
-                        // masked tokens have p = 0 and, their K rows being zero, a = 0
-                        const float p = fex2(dz[nt][x]);
-                        const float a = sc[u][nt][2 * (x & 1) + 1] * (Q8 ? fminf(afac[nt] * kscale[u], 3e38f) : afac[nt]);
-                        lsum[nt] += p;
-                        asum[nt] = fmaf(p, a, asum[nt]);
-                        w0 = p * vfac;
-                        w1 = w0 * (a * (1.f / ASCALE));
-                    } else {
-                        w0 = fex2(dz[2 * nt][x]);
-                        w1 = fex2(dz[2 * nt + 1][x]);
-                        lsum[2 * nt] += w0;
-                        lsum[2 * nt + 1] += w1;
-                        w0 *= vfac;
-                        w1 *= vfac;
-                    }
                     uint32_t hi, lo;
-                    split_pair<Q8>(w0, w1, hi, lo);
+                    if constexpr (RHO) {
+                        lsum[nt] += p[nt][x];
+                        asum[nt] = fmaf(p[nt][x], probe(nt, x), asum[nt]);
+                        split_pair<Q8>(wo[nt][x], wm[nt][x], hi, lo);
+                    } else {
+                        lsum[2 * nt] += p[2 * nt][x];
+                        lsum[2 * nt + 1] += p[2 * nt + 1][x];
+                        split_pair<Q8>(wo[2 * nt][x], wo[2 * nt + 1][x], hi, lo);
+                    }
                     bh[nt][x] = movmatrix(hi);
                     bl[nt][x] = movmatrix(lo);
                 }
@@ -690,7 +735,9 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                 }
             }
         }
-        const float oscale = Q8 ? exp2_whole(evref) : 1.f;
+        // O and M of head h as they are, for what the accumulators hold
+        auto of_o = [&](float v, int h) { return Q8 ? scaled(v, oexp[h] - WSHIFT) : v; };
+        auto of_m = [&](float v, int h) { return Q8 ? scaled(v, oexp[h] - whole_log2(mratio[h]) - WSHIFT) : v; };
         if (solo) {
             // the item is this warp's alone: the thread that holds a head's O[d] also holds its M[d]
             if (gave_up) return;
@@ -704,17 +751,17 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                     ab += __shfl_xor_sync(0xffffffffu, ab, off);
                 }
                 if (head >= nh) continue;
-                const float inv = 1.f / l, c = ab * inv, so = oscale * inv;
+                const float inv = 1.f / l, c = ab * inv;
                 Tout *yr = y + (h0 + head) * D;
 #pragma unroll
                 for (int j = 0; j < S::JS; ++j) {
                     const int d = Q8 || S::VB == 16 ? (S::VB / S::EL) * r + 2 * j : 64 * (j / 4) + 8 * r + 2 * (j % 4);
                     if constexpr (RHO) {
-                        const float o0 = oacc[nt][j][0] * so, o1 = oacc[nt][j][2] * so;
-                        store_y2(yr + d, o0 - (oacc[nt][j][1] * (so * ASCALE) - o0 * c),
-                                 o1 - (oacc[nt][j][3] * (so * ASCALE) - o1 * c));
+                        const float o0 = of_o(oacc[nt][j][0] * inv, h), o1 = of_o(oacc[nt][j][2] * inv, h);
+                        store_y2(yr + d, o0 - (of_m(oacc[nt][j][1] * inv, h) - o0 * c),
+                                 o1 - (of_m(oacc[nt][j][3] * inv, h) - o1 * c));
                     } else {
-                        store_y2(yr + d, oacc[nt][j][h % 2] * so, oacc[nt][j][2 + h % 2] * so);
+                        store_y2(yr + d, of_o(oacc[nt][j][h % 2] * inv, h), of_o(oacc[nt][j][2 + h % 2] * inv, h));
                     }
                 }
                 if (r == 0) {
@@ -752,13 +799,13 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
                 // rows r and r + 8 of the product's step j are elements d and d + 1
                 const int d = Q8 || S::VB == 16 ? (S::VB / S::EL) * r + 2 * j : 64 * (j / 4) + 8 * r + 2 * (j % 4);
                 if constexpr (RHO) {
-                    row[4 + d] = oacc[nt][j][0] * oscale;
-                    row[4 + d + 1] = oacc[nt][j][2] * oscale;
-                    row[4 + D + d] = oacc[nt][j][1] * (oscale * ASCALE);
-                    row[4 + D + d + 1] = oacc[nt][j][3] * (oscale * ASCALE);
+                    row[4 + d] = of_o(oacc[nt][j][0], h);
+                    row[4 + d + 1] = of_o(oacc[nt][j][2], h);
+                    row[4 + D + d] = of_m(oacc[nt][j][1], h);
+                    row[4 + D + d + 1] = of_m(oacc[nt][j][3], h);
                 } else {
-                    row[4 + d] = oacc[nt][j][h % 2] * oscale;
-                    row[4 + d + 1] = oacc[nt][j][2 + h % 2] * oscale;
+                    row[4 + d] = of_o(oacc[nt][j][h % 2], h);
+                    row[4 + d + 1] = of_o(oacc[nt][j][2 + h % 2], h);
                 }
             }
         }
