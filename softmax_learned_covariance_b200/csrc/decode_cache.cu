@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
             if constexpr (Q8) {
                 big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
                 big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                // bring the largest element to [2^7, 2^8)
-                const int up = min(max(134 - (int)(big >> 7), -110), 110);
+                // bring the largest element to [2^7, 2^8), or 2^120 closer: subnormal ones are exact there
+                const int up = min(max(134 - (int)(big >> 7), -120), 120);
                 const float f = exp2_whole(up);
                 inv = exp2_whole(-up);
 #pragma unroll

@@ -165,3 +165,15 @@ def test_probe_products_past_fp16(d, q8):
     rho[1] *= 2.0 ** 20
     rho[2] *= 2.0 ** 110
     check(c, bf16(q), bf16(rho), [320, 317, 200])
+
+
+@pytest.mark.parametrize("bits", [-130, -118, -100, 100, 118, 126])
+@pytest.mark.parametrize("d", [64, 128])
+def test_vectors_at_the_ends_of_their_type(d, bits):
+    """q and rho near bf16's largest and smallest values, under keys that bring their products back to 1."""
+    rng = np.random.default_rng(41)
+    c = Cache(rng, 3, 2, 16, 20, d)
+    k, v = (rng.standard_normal((c.n, 2, 16, d)) for _ in range(2))
+    refill(c, k * 2.0 ** min(-bits, 125), v)
+    q, rho = (rng.uniform(0.5, 1.9, (3, 6, d)) * rng.choice([-1.0, 1.0], (3, 6, d)) * s for s in (1.0, 0.1))
+    check(c, bf16(q * 2.0 ** bits), bf16(rho * 2.0 ** bits), [320, 317, 5])
