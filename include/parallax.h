@@ -358,7 +358,8 @@ PARALLAX_API int parallax_decode_paged_acc(const void *q, const void *rho, const
  *                 <= T; NULL for T each.
  *   new_seqlens : DEVICE int32 [B] or NULL (written: seqlens + counts); another
  *                 array than seqlens and counts (PARALLAX_ERR_UNSUPPORTED).
- *   wacc        : NULL, or the accumulator: the new tokens' entries become 0.
+ *   wacc        : NULL, or the accumulator: the new tokens' entries become 0 (also
+ *                 those of tokens that a bad page id drops, as they count in the length).
  *   Token t goes to row t % page_size of page block_table[b, t / page_size].
  *   8-bit cache: a block takes the smallest exponent e >= that of its rows that
  *   are there already with |x| <= 448 2^e for every new row; new rows are rounded

@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_append(KvAppendArgs A, unsign
     if (n == 0 || blk > (start + n - 1) / KV_BLOCK - start / KV_BLOCK) return;   // no new row
     const int p0 = (start / KV_BLOCK + blk) * KV_BLOCK;      // the block's first position
     const int lo = max(start - p0, 0), hi = min(start + n - p0, KV_BLOCK);   // its new rows
+    // the accumulator is the sequence's: its new entries are cleared whatever the page
+    if (A.wacc != nullptr && is_v && lane >= lo && lane < hi) A.wacc[(size_t)bk * cap + p0 + lane] = 0.f;
     const int id = A.pg.table[(size_t)b * A.pg.max_pages + (p0 >> A.pg.pshift)];
     if ((unsigned)id >= (unsigned)A.pg.num_pages) {
         if (lane == 0) atomicExch(err, PARALLAX_ERR_DEVICE_INDEX);
@@ -78,7 +80,6 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_append(KvAppendArgs A, unsign
     }
     const size_t slab = (size_t)id * A.pg.Hkv + kvh;
     const int row0 = p0 & (ps - 1);
-    if (A.wacc != nullptr && is_v && lane >= lo && lane < hi) A.wacc[(size_t)bk * cap + p0 + lane] = 0.f;
 
     const __nv_bfloat16 *x = is_v ? (const __nv_bfloat16 *)A.v : (const __nv_bfloat16 *)A.k;
     const long long sb = is_v ? A.v_stride[0] : A.k_stride[0], sh = is_v ? A.v_stride[1] : A.k_stride[1],

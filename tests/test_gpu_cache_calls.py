@@ -1,0 +1,31 @@
+"""The paged-cache calls beside their results: what they clear, what a failed one leaves, other threads."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import softmax_learned_covariance_b200 as plx
+from tests.test_gpu_cache import DEV, Cache, bf16, run_append
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("q8", [True, False])
+def test_append_clears_the_weights_of_tokens_on_bad_pages(q8):
+    """The accumulator belongs to the sequence: new tokens start at 0 there although their page is not written."""
+    rng = np.random.default_rng(50)
+    B, Hkv, T, d = 3, 2, 20, 64
+    c = Cache(rng, B, Hkv, 16, 3, d, q8)
+    c.table[1, 1] = c.n
+    c.table[2, 0] = -1
+    c.upload()
+    w = torch.ones((B, Hkv, 48), device=DEV)
+    k = bf16(rng.standard_normal((B, Hkv, T, d))).to(DEV)
+    ns = run_append(c, k, k, [5, 7, 0], [20, 20, 3], w)
+    assert ns.tolist() == [25, 27, 3]
+    assert plx.parallax_last_device_error() == 8
+    want = np.ones((B, Hkv, 48), np.float32)
+    for b, (s, n) in enumerate(((5, 20), (7, 20), (0, 3))):
+        want[b, :, s:s + n] = 0.0
+    assert np.array_equal(w.cpu().numpy(), want)
