@@ -44,27 +44,25 @@ std::mutex g_mu;
 DevState g_dev[MAX_DEVICES];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-int status_of(cudaError_t e) { return e == cudaSuccess ? PARALLAX_OK : PARALLAX_ERR_CUDA; }
-
 int get_state(DevState **out) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return PARALLAX_ERR_CUDA;
+    int dev = 0, st = PARALLAX_OK;
+    if ((st = status_of(cudaGetDevice(&dev)))) return st;
+    if (dev < 0 || dev >= MAX_DEVICES) return PARALLAX_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
     DevState &s = g_dev[dev];
     if (!s.init) {
-        if (cudaDeviceGetAttribute(&s.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return PARALLAX_ERR_CUDA;
-        if (cudaMalloc(&s.err, 256) != cudaSuccess) return PARALLAX_ERR_CUDA;
-        if (cudaMemset(s.err, 0, 256) != cudaSuccess) return PARALLAX_ERR_CUDA;
+        if ((st = status_of(cudaDeviceGetAttribute(&s.sms, cudaDevAttrMultiProcessorCount, dev)))) return st;
+        if ((st = status_of(cudaMalloc(&s.err, 256)))) return st;
+        if ((st = status_of(cudaMemset(s.err, 0, 256)))) return st;
         cudaMemPoolProps props;
         std::memset(&props, 0, sizeof(props));
         props.allocType = cudaMemAllocationTypePinned;
         props.handleTypes = cudaMemHandleTypeNone;
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
-        if (cudaMemPoolCreate(&s.pool, &props) != cudaSuccess) return PARALLAX_ERR_CUDA;
+        if ((st = status_of(cudaMemPoolCreate(&s.pool, &props)))) return st;
         unsigned long long keep = ~0ull;
-        if (cudaMemPoolSetAttribute(s.pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess)
-            return PARALLAX_ERR_CUDA;
+        if ((st = status_of(cudaMemPoolSetAttribute(s.pool, cudaMemPoolAttrReleaseThreshold, &keep)))) return st;
         s.init = true;
     }
     *out = &s;
@@ -86,9 +84,9 @@ class CallScratch {
     int get(size_t bytes, void **out) {
         *out = nullptr;
         if (bytes == 0) return PARALLAX_OK;
-        if (cudaMallocFromPoolAsync(&p_, bytes, s_->pool, st_) != cudaSuccess) {
+        if (int st = status_of(cudaMallocFromPoolAsync(&p_, bytes, s_->pool, st_))) {
             p_ = nullptr;
-            return PARALLAX_ERR_CUDA;
+            return st;
         }
         *out = p_;
         return PARALLAX_OK;
@@ -125,9 +123,8 @@ int ensure_encoder() {
     if (g_encode) return PARALLAX_OK;
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || fn == nullptr)
-        return PARALLAX_ERR_CUDA;
+    if (int st = status_of(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q))) return st;
+    if (q != cudaDriverEntryPointSuccess || fn == nullptr) return PARALLAX_ERR_CUDA;
     g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     return PARALLAX_OK;
 }
@@ -167,7 +164,7 @@ int prepare_fwd(const void *q, const void *k, const void *v, int B, int H, int T
     *counter = static_cast<int *>(ws);
     *vexp = static_cast<signed char *>(ws) + 256;
     void *v16 = static_cast<char *>(ws) + 256 + nexp;
-    if (launch_v_to_f16_blocks(v, v16, *vexp, B * H, T, d, cs) != cudaSuccess) return PARALLAX_ERR_CUDA;
+    if (int e = status_of(launch_v_to_f16_blocks(v, v16, *vexp, B * H, T, d, cs))) return e;
     const uint64_t dims[3] = {(uint64_t)d, (uint64_t)T, (uint64_t)B * H};
     // boxes: 64 head-dim columns (128 B, the swizzle span) x {128 query rows, 128 keys, 64 keys}
     const uint32_t box_q[3] = {64, 128, 1}, box_k[3] = {64, 128, 1}, box_v[3] = {64, 64, 1};
@@ -208,14 +205,14 @@ int parallax_last_device_error(parallax_stream_t stream) {
     DevState *s = nullptr;
     int st = get_state(&s);
     if (st) return st;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PARALLAX_ERR_CUDA;
+    if ((st = status_of(cudaStreamSynchronize(static_cast<cudaStream_t>(stream))))) return st;
     int v = 0;
-    if (cudaMemcpy(&v, s->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return PARALLAX_ERR_CUDA;
-    if (v != 0 && cudaMemset(s->err, 0, sizeof(int)) != cudaSuccess) return PARALLAX_ERR_CUDA;
+    if ((st = status_of(cudaMemcpy(&v, s->err, sizeof(int), cudaMemcpyDeviceToHost)))) return st;
+    if (v != 0 && (st = status_of(cudaMemset(s->err, 0, sizeof(int))))) return st;
     if (int *w = noalloc_error_word()) {
         int v2 = 0;
-        if (cudaMemcpy(&v2, w, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return PARALLAX_ERR_CUDA;
-        if (v2 != 0 && cudaMemset(w, 0, sizeof(int)) != cudaSuccess) return PARALLAX_ERR_CUDA;
+        if ((st = status_of(cudaMemcpy(&v2, w, sizeof(int), cudaMemcpyDeviceToHost)))) return st;
+        if (v2 != 0 && (st = status_of(cudaMemset(w, 0, sizeof(int))))) return st;
         if (v == 0) v = v2;
     }
     return v;

@@ -55,11 +55,11 @@ int noalloc_setup(int dev, NoallocDevice **out) {
     NoallocDevice &s = g_noalloc_dev[dev];
     if (!s.ready) {
         void *p = nullptr, *e = nullptr;
-        if (cudaGetSymbolAddress(&p, g_decode_scratch) != cudaSuccess || p == nullptr) return PARALLAX_ERR_CUDA;
-        if (cudaGetSymbolAddress(&e, g_noalloc_err) != cudaSuccess || e == nullptr) return PARALLAX_ERR_CUDA;
-        int sms = 0;
-        if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-            return PARALLAX_ERR_CUDA;
+        int sms = 0, st = PARALLAX_OK;
+        if ((st = plx::status_of(cudaGetSymbolAddress(&p, g_decode_scratch)))) return st;
+        if ((st = plx::status_of(cudaGetSymbolAddress(&e, g_noalloc_err)))) return st;
+        if ((st = plx::status_of(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))) return st;
+        if (p == nullptr || e == nullptr || sms <= 0) return PARALLAX_ERR_CUDA;
         s.scratch = p;
         s.err = static_cast<int *>(e);
         s.sms = sms;
@@ -73,7 +73,7 @@ int noalloc_setup(int dev, NoallocDevice **out) {
 
 int *plx::noalloc_error_word() {
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    if (plx::status_of(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return nullptr;
     std::lock_guard<std::mutex> lk(g_noalloc_mu);
     return g_noalloc_dev[dev].ready ? g_noalloc_dev[dev].err : nullptr;
 }
@@ -98,7 +98,7 @@ extern "C" PARALLAX_API int parallax_decode_noalloc(const void *q, const void *r
         return PARALLAX_ERR_DTYPE;
 
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PARALLAX_ERR_CUDA;
+    if (plx::status_of(cudaGetDevice(&dev)) || dev < 0 || dev >= kMaxDevices) return PARALLAX_ERR_CUDA;
     NoallocDevice *s = nullptr;
     if (int st = noalloc_setup(dev, &s)) return st;
 
@@ -109,5 +109,5 @@ extern "C" PARALLAX_API int parallax_decode_noalloc(const void *q, const void *r
     const cudaError_t e = plx::launch_decode(q, rho, kcache, vcache, seqlens, y, lse, B, H, Tcap, d, out_dtype, plan,
                                              static_cast<float *>(s->scratch), s->sms, plx::ctl_from_env(s->err),
                                              static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PARALLAX_OK : PARALLAX_ERR_CUDA;
+    return plx::status_of(e);
 }

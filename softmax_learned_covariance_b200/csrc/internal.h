@@ -25,6 +25,15 @@ template <typename F> cudaError_t ensure_smem_limit(F f, int bytes, std::atomic<
     return e;
 }
 
+// A runtime call's result as a status.  An error that is reported does not stay
+// behind as the runtime's last error, where the check after the next call's launch
+// would find it and report that call as failed.
+inline int status_of(cudaError_t e) {
+    if (e == cudaSuccess) return PARALLAX_OK;
+    cudaGetLastError();
+    return PARALLAX_ERR_CUDA;
+}
+
 // Per-launch wait policy: absolute %globaltimer deadline is computed in-kernel
 // from this budget (nanoseconds).
 struct DeviceCtl {

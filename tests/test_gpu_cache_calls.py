@@ -1,12 +1,14 @@
 """The paged-cache calls beside their results: what they clear, what a failed one leaves, other threads."""
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import softmax_learned_covariance_b200 as plx
-from tests.test_gpu_cache import DEV, Cache, bf16, run_append
+from tests.test_gpu_cache import DEV, Cache, bf16, no_error, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +31,27 @@ def test_append_clears_the_weights_of_tokens_on_bad_pages(q8):
     for b, (s, n) in enumerate(((5, 20), (7, 20), (0, 3))):
         want[b, :, s:s + n] = 0.0
     assert np.array_equal(w.cpu().numpy(), want)
+
+
+def test_a_call_that_fails_leaves_nothing_to_the_next():
+    """Scores for 2^35 table slots (a terabyte) cannot be had: that call reports it, the next one is a success."""
+    rng = np.random.default_rng(51)
+    c = Cache(rng, 2, 2, 16, 4, 64)
+    q = bf16(rng.standard_normal((2, 16, 64))).to(DEV)
+    sl = torch.tensor([64, 10] + [0] * 14, dtype=torch.int32, device=DEV)
+    w = torch.zeros((2, 2, 64), device=DEV)
+    y = torch.empty((2, 16, 64), device=DEV)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    L = plx.lib()
+
+    def call(mp, B, Hkv, Hq):
+        return L.parallax_decode_paged_q8(p(q), None, p(c.kp), p(c.vp), p(c.ke), p(c.ve), p(c.tab), p(sl), p(y), None,
+                                          p(w), B, Hq, Hkv, 16, mp, c.n, 64, plx.BF16, plx.F32,
+                                          ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert call(4, 2, 2, 16) == 0
+    ok = y.clone()
+    assert call(1 << 26, 16, 2, 16) == 6             # no launch: the scratch comes first
+    y.zero_()
+    assert call(4, 2, 2, 16) == 0
+    assert torch.equal(y, ok)
+    no_error()
