@@ -158,7 +158,8 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
         out_type = reinterpret_cast<THPDtype *>(a[11])->scalar_type;
         TORCH_CHECK_TYPE(out_type == at::kFloat || out_type == at::kBFloat16, "unsupported dtype ", out_type);
     }
-    const bool want_q8 = a[13] == Py_True;
+    const bool want_q8 = a[13] == Py_True, want_lse = PyObject_IsTrue(a[12]) == 1;
+    if (PyErr_Occurred()) return nullptr;
     TORCH_CHECK_TYPE(tensor(a[2], "kpages").scalar_type() == (want_q8 ? at::kFloat8_e4m3fn : at::kBFloat16),
                      "kpages must be ", want_q8 ? "float8_e4m3fn" : "bfloat16");
     const Cache c = cache(a[2], a[3], a[4], a[5], a[6], a[7]);
@@ -179,7 +180,7 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (lse.defined())
         is(lse, "lse", at::kFloat, {c.B, Hq}, c.dev);
-    else if (PyObject_IsTrue(a[12]) == 1)
+    else if (want_lse)
         lse = fresh({c.B, Hq}, at::kFloat, c.dev);
     const int out = y.scalar_type() == at::kFloat ? PARALLAX_F32 : PARALLAX_BF16;
     const int B = (int)c.B, hq = small(Hq, "Hq"), hkv = (int)c.Hkv, ps = small(c.ps, "page_size"), d = small(c.d, "d");
