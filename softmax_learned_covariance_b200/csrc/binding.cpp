@@ -136,6 +136,17 @@ PyObject *tuple(std::initializer_list<PyObject *> items) {
     return t;
 }
 
+// Other Python threads run while this one allocates and calls the library: either may
+// wait there (for room in the launch queue, whose head may be a host callback that
+// needs the interpreter), and torch's own calls and the ctypes ones let them as well.
+struct NoGil {
+    PyThreadState *state = PyEval_SaveThread();
+    NoGil() = default;
+    NoGil(const NoGil &) = delete;
+    NoGil &operator=(const NoGil &) = delete;
+    ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 bool count(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return true;
     PyErr_Format(PyExc_TypeError, "%zd arguments are wanted, not %zd", want, n);
@@ -171,25 +182,29 @@ PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (rho.defined()) is(rho, "rho", at::kBFloat16, shape, c.dev);
     if (wacc.defined()) is(wacc, "wacc", at::kFloat, {c.B, c.Hkv, c.mp * c.ps}, c.dev);
     TORCH_CHECK_VALUE(c.q8 || wacc.defined(), "wacc is required; without it use parallax_decode_paged");
-    const c10::cuda::CUDAGuard guard(c.dev);
-    if (y.defined()) {
-        TORCH_CHECK_TYPE(y.scalar_type() == at::kFloat || y.scalar_type() == at::kBFloat16, "unsupported dtype of y");
-        is(y, "y", y.scalar_type(), shape, c.dev);
-    } else {
-        y = fresh(shape, out_type, c.dev);
-    }
-    if (lse.defined())
-        is(lse, "lse", at::kFloat, {c.B, Hq}, c.dev);
-    else if (want_lse)
-        lse = fresh({c.B, Hq}, at::kFloat, c.dev);
-    const int out = y.scalar_type() == at::kFloat ? PARALLAX_F32 : PARALLAX_BF16;
     const int B = (int)c.B, hq = small(Hq, "Hq"), hkv = (int)c.Hkv, ps = small(c.ps, "page_size"), d = small(c.d, "d");
-    const int st = c.q8 ? g_q8(at_(q), at_(rho), at_(c.k), at_(c.v), at_<signed char>(c.kexp), at_<signed char>(c.vexp),
-                               at_<int>(c.table), at_<int>(c.seqlens), at_(y), at_<float>(lse), at_<float>(wacc), B, hq,
-                               hkv, ps, (int)c.mp, (int)c.np, d, PARALLAX_BF16, out, stream_of(c.dev))
-                        : g_acc(at_(q), at_(rho), at_(c.k), at_(c.v), at_<int>(c.table), at_<int>(c.seqlens), at_(y),
-                                at_<float>(lse), at_<float>(wacc), B, hq, hkv, ps, (int)c.mp, (int)c.np, d,
-                                PARALLAX_BF16, out, stream_of(c.dev));
+    int st;
+    {
+        const NoGil no_gil;
+        const c10::cuda::CUDAGuard guard(c.dev);
+        if (y.defined()) {
+            TORCH_CHECK_TYPE(y.scalar_type() == at::kFloat || y.scalar_type() == at::kBFloat16, "unsupported dtype of y");
+            is(y, "y", y.scalar_type(), shape, c.dev);
+        } else {
+            y = fresh(shape, out_type, c.dev);
+        }
+        if (lse.defined())
+            is(lse, "lse", at::kFloat, {c.B, Hq}, c.dev);
+        else if (want_lse)
+            lse = fresh({c.B, Hq}, at::kFloat, c.dev);
+        const int out = y.scalar_type() == at::kFloat ? PARALLAX_F32 : PARALLAX_BF16;
+        st = c.q8 ? g_q8(at_(q), at_(rho), at_(c.k), at_(c.v), at_<signed char>(c.kexp), at_<signed char>(c.vexp),
+                         at_<int>(c.table), at_<int>(c.seqlens), at_(y), at_<float>(lse), at_<float>(wacc), B, hq,
+                         hkv, ps, (int)c.mp, (int)c.np, d, PARALLAX_BF16, out, stream_of(c.dev))
+                  : g_acc(at_(q), at_(rho), at_(c.k), at_(c.v), at_<int>(c.table), at_<int>(c.seqlens), at_(y),
+                          at_<float>(lse), at_<float>(wacc), B, hq, hkv, ps, (int)c.mp, (int)c.np, d,
+                          PARALLAX_BF16, out, stream_of(c.dev));
+    }
     if (st) return PyLong_FromLong(st);
     return tuple({wrap(y), wrap(lse)});
     END_HANDLE_TH_ERRORS
@@ -217,16 +232,20 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (counts.defined()) is(counts, "counts", at::kInt, {c.B}, c.dev);
     if (wacc.defined()) is(wacc, "wacc", at::kFloat, {c.B, c.Hkv, c.mp * c.ps}, c.dev);
-    const c10::cuda::CUDAGuard guard(c.dev);
-    if (lens.defined())
-        is(lens, "new_seqlens", at::kInt, {c.B}, c.dev);
-    else
-        lens = fresh({c.B}, at::kInt, c.dev);
-    const int st = g_append(at_(x[0]), at_(x[1]), strides[0], strides[1], at_(c.k), at_(c.v), at_<signed char>(c.kexp),
-                            at_<signed char>(c.vexp), at_<int>(c.table), at_<int>(c.seqlens), at_<int>(counts),
-                            at_<int>(lens), at_<float>(wacc), (int)c.B, (int)c.Hkv, small(T, "T"),
-                            small(c.ps, "page_size"), (int)c.mp, (int)c.np, small(c.d, "d"), PARALLAX_BF16,
-                            c.q8 ? PARALLAX_E4M3 : PARALLAX_BF16, stream_of(c.dev));
+    const int t = small(T, "T"), ps = small(c.ps, "page_size"), d = small(c.d, "d");
+    int st;
+    {
+        const NoGil no_gil;
+        const c10::cuda::CUDAGuard guard(c.dev);
+        if (lens.defined())
+            is(lens, "new_seqlens", at::kInt, {c.B}, c.dev);
+        else
+            lens = fresh({c.B}, at::kInt, c.dev);
+        st = g_append(at_(x[0]), at_(x[1]), strides[0], strides[1], at_(c.k), at_(c.v), at_<signed char>(c.kexp),
+                      at_<signed char>(c.vexp), at_<int>(c.table), at_<int>(c.seqlens), at_<int>(counts),
+                      at_<int>(lens), at_<float>(wacc), (int)c.B, (int)c.Hkv, t, ps, (int)c.mp, (int)c.np, d,
+                      PARALLAX_BF16, c.q8 ? PARALLAX_E4M3 : PARALLAX_BF16, stream_of(c.dev));
+    }
     if (st) return PyLong_FromLong(st);
     return wrap(lens);
     END_HANDLE_TH_ERRORS
@@ -248,24 +267,28 @@ PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     is(table, "new_table", at::kInt, {c.B, nmp}, c.dev);
     TORCH_CHECK_VALUE(1 <= budget && budget <= nmp * c.ps && 0 <= recent && recent <= budget,
                       "1 <= budget <= new_max_pages * page_size and 0 <= recent <= budget are wanted");
-    const c10::cuda::CUDAGuard guard(c.dev);
-    if (lens.defined())
-        is(lens, "new_seqlens", at::kInt, {c.B}, c.dev);
-    else
-        lens = fresh({c.B}, at::kInt, c.dev);
-    if (kept.defined())
-        is(kept, "kept", at::kInt, {c.B, c.Hkv, (int64_t)budget}, c.dev);
-    else
-        kept = fresh({c.B, c.Hkv, (int64_t)budget}, at::kInt, c.dev).zero_();
-    if (nw.defined())
-        is(nw, "new_wacc", at::kFloat, {c.B, c.Hkv, nmp * c.ps}, c.dev);
-    else
-        nw = fresh({c.B, c.Hkv, nmp * c.ps}, at::kFloat, c.dev).zero_();
-    const int st = g_evict(at_(c.k), at_(c.v), at_<signed char>(c.kexp), at_<signed char>(c.vexp), at_<int>(c.table),
-                           at_<int>(c.seqlens), at_<float>(wacc), at_<int>(table), at_<int>(lens), at_<int>(kept),
-                           at_<float>(nw), (int)c.B, (int)c.Hkv, small(c.ps, "page_size"), (int)c.mp,
-                           small(nmp, "new_max_pages"), (int)c.np, small(c.d, "d"), (int)budget, (int)recent,
-                           c.q8 ? PARALLAX_E4M3 : PARALLAX_BF16, stream_of(c.dev));
+    const int ps = small(c.ps, "page_size"), nmax = small(nmp, "new_max_pages"), d = small(c.d, "d");
+    int st;
+    {
+        const NoGil no_gil;
+        const c10::cuda::CUDAGuard guard(c.dev);
+        if (lens.defined())
+            is(lens, "new_seqlens", at::kInt, {c.B}, c.dev);
+        else
+            lens = fresh({c.B}, at::kInt, c.dev);
+        if (kept.defined())
+            is(kept, "kept", at::kInt, {c.B, c.Hkv, (int64_t)budget}, c.dev);
+        else
+            kept = fresh({c.B, c.Hkv, (int64_t)budget}, at::kInt, c.dev).zero_();
+        if (nw.defined())
+            is(nw, "new_wacc", at::kFloat, {c.B, c.Hkv, nmp * c.ps}, c.dev);
+        else
+            nw = fresh({c.B, c.Hkv, nmp * c.ps}, at::kFloat, c.dev).zero_();
+        st = g_evict(at_(c.k), at_(c.v), at_<signed char>(c.kexp), at_<signed char>(c.vexp), at_<int>(c.table),
+                     at_<int>(c.seqlens), at_<float>(wacc), at_<int>(table), at_<int>(lens), at_<int>(kept),
+                     at_<float>(nw), (int)c.B, (int)c.Hkv, ps, (int)c.mp, nmax, (int)c.np, d, (int)budget, (int)recent,
+                     c.q8 ? PARALLAX_E4M3 : PARALLAX_BF16, stream_of(c.dev));
+    }
     if (st) return PyLong_FromLong(st);
     return tuple({wrap(lens), wrap(kept), wrap(nw)});
     END_HANDLE_TH_ERRORS

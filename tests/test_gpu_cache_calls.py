@@ -2,6 +2,10 @@
 from __future__ import annotations
 
 import ctypes
+import shutil
+import subprocess
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -55,3 +59,54 @@ def test_a_call_that_fails_leaves_nothing_to_the_next():
     assert call(4, 2, 2, 16) == 0
     assert torch.equal(y, ok)
     no_error()
+
+
+def test_other_python_threads_run_during_a_call(tmp_path):
+    """A call that waits inside the library (here a stand-in that sleeps) does not hold the interpreter."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no g++")
+    src = tmp_path / "slow.cpp"
+    src.write_text('#include <unistd.h>\nextern "C" int slow() { usleep(400000); return 0; }\n')
+    so = str(tmp_path / "slow.so")
+    subprocess.check_call([gxx, "-shared", "-fPIC", "-o", so, str(src)])
+    slow = ctypes.cast(ctypes.CDLL(so).slow, ctypes.c_void_p).value
+    rng = np.random.default_rng(52)
+    c = Cache(rng, 1, 2, 16, 2, 64, more=1)
+    q = bf16(rng.standard_normal((1, 2, 64))).to(DEV)
+    k = bf16(rng.standard_normal((1, 2, 1, 64))).to(DEV)
+    sl = torch.tensor([16], dtype=torch.int32, device=DEV)
+    w = torch.zeros((1, 2, 32), device=DEV)
+    calls = [lambda: plx.parallax_decode_paged_q8(q, None, c.kp, c.vp, c.ke, c.ve, c.tab, sl),
+             lambda: plx.parallax_kv_append(k, k, c.kp, c.vp, c.tab, sl, kexp=c.ke, vexp=c.ve),
+             lambda: plx.parallax_kv_evict(c.kp, c.vp, c.tab, sl, w, c.tab2, 8, 0, kexp=c.ke, vexp=c.ve)]
+    for f in calls:
+        f()
+    torch.cuda.synchronize()
+    L = plx.lib()
+    real = [ctypes.cast(f, ctypes.c_void_p).value for f in
+            (L.parallax_decode_paged_q8, L.parallax_decode_paged_acc, L.parallax_kv_append, L.parallax_kv_evict)]
+    stop, beats = threading.Event(), []
+
+    def beat():
+        while not stop.is_set():
+            beats.append(time.monotonic())
+            time.sleep(0.005)
+
+    thread = threading.Thread(target=beat)
+    native = plx._native()
+    native.bind(slow, slow, slow, slow)
+    try:
+        thread.start()
+        seen = []
+        for f in calls:
+            start = time.monotonic()
+            f()
+            end = time.monotonic()
+            assert end - start >= 0.39
+            seen.append(sum(start + 0.05 < t < end - 0.05 for t in list(beats)))
+    finally:
+        stop.set()
+        thread.join()
+        native.bind(*real)
+    assert min(seen) >= 5                            # 60 beats of 5 ms fit, none while the interpreter is held
