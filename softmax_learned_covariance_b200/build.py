@@ -7,17 +7,21 @@ header changed) and the objects are linked into a shared library next to this
 file.  The CUDA runtime is linked statically so the library loads wherever the
 NVIDIA driver is present; the driver API entry point for TMA descriptors is
 resolved at run time.  csrc/binding.cpp, the native part of the Python binding,
-becomes the extension module _binding.so next to it (g++ against torch's headers).
+becomes the extension module _binding.so next to it (g++ against torch's headers; the
+library itself does not need torch and is built without it as well).
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -52,12 +56,28 @@ def _stale(src, obj, newest_header):
     return os.path.getmtime(src) > t or newest_header > t
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    header = os.path.join(INCLUDE, "parallax.h")
-    if not force and not _stale(BINDING_SRC, BINDING, os.path.getmtime(header)):
-        return BINDING
-    import sysconfig
+def _built_against():
+    """What _binding.so fits, as text: this torch and this Python; None without torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "?"
+    return f"torch {version} {spec.origin} python {sysconfig.get_config_var('EXT_SUFFIX')}\n"
 
+
+def build_binding(force: bool = False, verbose: bool = False) -> str | None:
+    fits = _built_against()
+    if fits is None:
+        print("torch is not installed: the library is built, its Python binding is not", file=sys.stderr)
+        return None
+    header = os.path.join(INCLUDE, "parallax.h")
+    stamp = os.path.join(BUILD, "binding.txt")
+    fresh = os.path.exists(stamp) and open(stamp).read() == fits
+    if not force and fresh and not _stale(BINDING_SRC, BINDING, os.path.getmtime(header)):
+        return BINDING
     import torch
     from torch.utils import cpp_extension
 
@@ -76,6 +96,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(r.stdout + r.stderr, file=sys.stderr)
         raise RuntimeError("g++ failed for: " + BINDING_SRC)
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(fits)
     return BINDING
 
 
