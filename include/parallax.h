@@ -356,8 +356,8 @@ PARALLAX_API int parallax_decode_paged_acc(const void *q, const void *rho, const
  *   seqlens     : DEVICE int32 [B], tokens already in the cache.
  *   counts      : DEVICE int32 [B], new tokens of each sequence, 0 <= counts[b]
  *                 <= T; NULL for T each.
- *   new_seqlens : DEVICE int32 [B] or NULL (written: seqlens + counts); another
- *                 array than seqlens and counts (PARALLAX_ERR_UNSUPPORTED).
+ *   new_seqlens : DEVICE int32 [B] or NULL (written: seqlens + counts); no part of
+ *                 seqlens or counts (PARALLAX_ERR_UNSUPPORTED).
  *   wacc        : NULL, or the accumulator: the new tokens' entries become 0 (also
  *                 those of tokens that a bad page id drops, as they count in the length).
  *   Token t goes to row t % page_size of page block_table[b, t / page_size].
@@ -365,7 +365,8 @@ PARALLAX_API int parallax_decode_paged_acc(const void *q, const void *rho, const
  *   are there already with |x| <= 448 2^e for every new row; new rows are rounded
  *   to nearest even, rows that are there are moved to e (exact while their code
  *   does not become subnormal).  An element that is not finite is stored as NaN
- *   and does not enter e.
+ *   and does not enter e.  K and V have pages and exponents of their own
+ *   (PARALLAX_ERR_UNSUPPORTED).
  *   Rows of no new token are not touched.  Tokens past max_pages * page_size are
  *   dropped, and tokens of a page id outside [0, num_pages) too; both set
  *   PARALLAX_ERR_DEVICE_INDEX in the device error word.  No scratch.
@@ -397,8 +398,8 @@ PARALLAX_API int parallax_kv_append(const void *k, const void *v, const long lon
  *   8-bit cache: a new block takes the largest exponent of its rows' old blocks.
  *   Rows past n are not touched.  A row of a page id outside [0, num_pages) is
  *   kept as zero, a new page outside it is not written; both set
- *   PARALLAX_ERR_DEVICE_INDEX.  new_seqlens, new_wacc and new_table equal to
- *   their counterparts: PARALLAX_ERR_UNSUPPORTED.  No scratch.
+ *   PARALLAX_ERR_DEVICE_INDEX.  new_seqlens or new_wacc with a part of its
+ *   counterpart, new_table equal to it: PARALLAX_ERR_UNSUPPORTED.  No scratch.
  */
 PARALLAX_API int parallax_kv_evict(void *kpages, void *vpages, signed char *kexp, signed char *vexp,
                                    const int *block_table, const int *seqlens, const float *wacc,

@@ -469,6 +469,12 @@ int paged_layout(const int *table, int B, int Hkv, int page_size, int max_pages,
     return PARALLAX_OK;
 }
 
+// whether two arrays have a byte in common (no array: none)
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
+
 // e4m3 caches have both exponent arrays, bf16 caches none.
 int cache_dtype_ok(int dtype, const void *kexp, const void *vexp) {
     if (dtype == PARALLAX_E4M3) return kexp && vexp ? PARALLAX_OK : PARALLAX_ERR_NULL;
@@ -556,7 +562,12 @@ int parallax_kv_append(const void *k, const void *v, const long long *k_strides,
         (wacc && !aligned16(wacc)))
         return PARALLAX_ERR_ALIGN;
     // other blocks of the launch still read the old lengths
-    if (new_seqlens && (new_seqlens == seqlens || new_seqlens == counts)) return PARALLAX_ERR_UNSUPPORTED;
+    const size_t ints = (size_t)B * sizeof(int);
+    if (overlap(new_seqlens, ints, seqlens, ints) || overlap(new_seqlens, ints, counts, ints))
+        return PARALLAX_ERR_UNSUPPORTED;
+    // K and V of a block are written by two warps, which both move the rows that are there
+    const size_t codes = (size_t)num_pages * Hkv * page_size * d, exps = (size_t)num_pages * Hkv * (page_size / 16);
+    if (kexp && (overlap(kpages, codes, vpages, codes) || overlap(kexp, exps, vexp, exps))) return PARALLAX_ERR_UNSUPPORTED;
     DevState *s = nullptr;
     if ((st = get_state(&s))) return st;
     return status_of(launch_kv_append(A, make_ctl(s), static_cast<cudaStream_t>(stream)));
@@ -581,7 +592,10 @@ int parallax_kv_evict(void *kpages, void *vpages, signed char *kexp, signed char
         !aligned4(new_table) || !aligned4(new_seqlens) || !aligned4(kept) || (new_wacc && !aligned16(new_wacc)))
         return PARALLAX_ERR_ALIGN;
     // the move reads what the source table names while it writes: nothing in place
-    if (new_table == block_table || new_seqlens == seqlens || new_wacc == wacc) return PARALLAX_ERR_UNSUPPORTED;
+    const size_t ints = (size_t)B * sizeof(int), row = (size_t)B * Hkv * page_size * sizeof(float);
+    if (new_table == block_table || overlap(new_seqlens, ints, seqlens, ints) ||
+        overlap(new_wacc, row * new_max_pages, wacc, row * max_pages))
+        return PARALLAX_ERR_UNSUPPORTED;
     DevState *s = nullptr;
     if ((st = get_state(&s))) return st;
     return status_of(launch_kv_evict(A, s->sms, make_ctl(s), static_cast<cudaStream_t>(stream)));

@@ -110,3 +110,29 @@ def test_other_python_threads_run_during_a_call(tmp_path):
         thread.join()
         native.bind(*real)
     assert min(seen) >= 5                            # 60 beats of 5 ms fit, none while the interpreter is held
+
+
+def test_arrays_beside_one_another_are_not_over_one_another():
+    """Lengths, exponents and accumulators that are parts of one buffer each, next to each other."""
+    rng = np.random.default_rng(53)
+    B, Hkv, ps, mp, d = 4, 2, 16, 3, 64
+    c = Cache(rng, B, Hkv, ps, mp, d, more=1)
+    k = bf16(rng.standard_normal((B, Hkv, 5, d))).to(DEV)
+    sl = torch.tensor([0, 7, 16, 40], dtype=torch.int32, device=DEV)
+    w = torch.rand((B, Hkv, mp * ps), device=DEV)
+
+    def serve(kp, vp, ke, ve, lens, sl, ns, w, nw):
+        plx.parallax_kv_append(k, k, kp, vp, c.tab, sl, kexp=ke, vexp=ve, new_seqlens=ns, wacc=w)
+        plx.parallax_kv_evict(kp, vp, c.tab, ns, w, c.tab2, 16, 2, kexp=ke, vexp=ve, new_seqlens=lens, new_wacc=nw)
+        return [t.clone() for t in (kp.view(torch.uint8), vp.view(torch.uint8), ke, ve, lens, ns, w, nw)]
+
+    apart = serve(c.kp.clone(), c.vp.clone(), c.ke.clone(), c.ve.clone(), torch.zeros_like(sl), sl.clone(),
+                  torch.zeros_like(sl), w.clone(), torch.zeros((B, Hkv, ps), device=DEV))
+    pages, exps = torch.stack([c.kp.view(torch.uint8), c.vp.view(torch.uint8)]).view(c.kp.dtype), torch.stack([c.ke, c.ve])
+    lens = torch.stack([torch.zeros_like(sl), sl, torch.zeros_like(sl)])
+    both = torch.cat([w.flatten(), torch.zeros(B * Hkv * ps, device=DEV)])
+    beside = serve(pages[0], pages[1], exps[0], exps[1], lens[0], lens[1], lens[2], both[:w.numel()].view_as(w),
+                   both[w.numel():].view(B, Hkv, ps))
+    for a, b in zip(apart, beside):
+        assert torch.equal(a, b)
+    no_error()
