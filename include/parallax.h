@@ -46,6 +46,8 @@
  *     may still use it.  The pool keeps returned memory for later calls.
  *     parallax_decode_ex (caller's workspace) and parallax_decode_noalloc
  *     (static array) do not use the pool.
+ *   - Calls may be captured into CUDA graphs, a process's first one too
+ *     (parallax_decode_noalloc says what it needs before that).
  */
 #ifndef PARALLAX_H
 #define PARALLAX_H

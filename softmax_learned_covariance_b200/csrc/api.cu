@@ -44,6 +44,30 @@ std::mutex g_mu;
 DevState g_dev[MAX_DEVICES];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
+// While one lives, this thread may allocate although a stream is being captured: what
+// the library sets up once per device is no part of anybody's graph.
+class RelaxedCapture {
+  public:
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    RelaxedCapture(const RelaxedCapture &) = delete;
+    RelaxedCapture &operator=(const RelaxedCapture &) = delete;
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+
+  private:
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
+// Zeroes device memory now, on a stream that no other stream waits for (the default
+// stream may not be used while a blocking one is captured).
+int zero_now(void *p, size_t bytes) {
+    cudaStream_t s = nullptr;
+    if (int st = status_of(cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking))) return st;
+    int st = status_of(cudaMemsetAsync(p, 0, bytes, s));
+    if (st == PARALLAX_OK) st = status_of(cudaStreamSynchronize(s));
+    cudaStreamDestroy(s);
+    return st;
+}
+
 int get_state(DevState **out) {
     int dev = 0, st = PARALLAX_OK;
     if ((st = status_of(cudaGetDevice(&dev)))) return st;
@@ -51,9 +75,10 @@ int get_state(DevState **out) {
     std::lock_guard<std::mutex> lk(g_mu);
     DevState &s = g_dev[dev];
     if (!s.init) {
+        const RelaxedCapture relaxed;
         if ((st = status_of(cudaDeviceGetAttribute(&s.sms, cudaDevAttrMultiProcessorCount, dev)))) return st;
-        if ((st = status_of(cudaMalloc(&s.err, 256)))) return st;
-        if ((st = status_of(cudaMemset(s.err, 0, 256)))) return st;
+        if (s.err == nullptr && (st = status_of(cudaMalloc(&s.err, 256)))) return st;
+        if ((st = zero_now(s.err, 256))) return st;
         cudaMemPoolProps props;
         std::memset(&props, 0, sizeof(props));
         props.allocType = cudaMemAllocationTypePinned;

@@ -2,8 +2,10 @@
 from __future__ import annotations
 
 import ctypes
+import os
 import shutil
 import subprocess
+import sys
 import threading
 import time
 
@@ -136,3 +138,46 @@ def test_arrays_beside_one_another_are_not_over_one_another():
     for a, b in zip(apart, beside):
         assert torch.equal(a, b)
     no_error()
+
+
+FIRST_CALL = """
+import sys
+import torch
+import softmax_learned_covariance_b200 as plx
+gen = torch.Generator(device="cuda:0").manual_seed(1)
+rand = lambda *shape: torch.randn(shape, device="cuda:0", generator=gen)
+ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda:0")
+pages = [rand(8, 2, 16, 64) for _ in range(2)]
+k8, v8 = (x.to(torch.float8_e4m3fn) for x in pages)
+kb, vb = (x.to(torch.bfloat16) for x in pages)
+ke, ve = (torch.zeros((8, 2, 1), dtype=torch.int8, device="cuda:0") for _ in range(2))
+table, new_table, sl = ints(*range(6)).view(2, 3), ints(6, 7).view(2, 1), ints(40, 17)
+q, k, w = rand(2, 8, 64).to(torch.bfloat16), rand(2, 2, 3, 64).to(torch.bfloat16), rand(2, 2, 48).abs()
+call = {
+    "append": lambda: (plx.parallax_kv_append(k, k, k8, v8, table, sl, kexp=ke, vexp=ve), k8.view(torch.uint8)),
+    "decode": lambda: (*plx.parallax_decode_paged_q8(q, q, k8, v8, ke, ve, table, sl, wacc=w), w),
+    "evict": lambda: plx.parallax_kv_evict(k8, v8, table, sl, w, new_table, 16, 3, kexp=ke, vexp=ve),
+    "paged": lambda: plx.parallax_decode_paged(q, q, kb, vb, table, sl),
+}[sys.argv[1]]
+state = [t.clone() for t in (k8.view(torch.uint8), v8.view(torch.uint8), ke, ve, w)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = call()
+graph.replay()
+got = [t.clone() for t in out]
+for t, s in zip((k8.view(torch.uint8), v8.view(torch.uint8), ke, ve, w), state):
+    t.copy_(s)
+for a, b in zip(got, call()):
+    assert torch.equal(a, b)
+assert plx.parallax_last_device_error() == 0
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("op", ["append", "decode", "evict", "paged"])
+def test_the_first_call_of_a_process_may_be_captured(op):
+    """What the library sets up on a device is no part of the capture and does not end it."""
+    here = os.path.dirname(os.path.dirname(os.path.abspath(plx.__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL, op], cwd=here, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stdout + r.stderr
