@@ -330,7 +330,9 @@ PARALLAX_API int parallax_decode_noalloc(const void *q, const void *rho, const v
  * is more (bf16 cache: 2^-16 of it); the other sums are fp32.
  * Results do not depend on the schedule (no atomics).  Scratch: split partials,
  * and with wacc 4 bytes per (sequence, token slot of the table, query head
- * rounded up to a multiple of 4, of 8 without rho or above 4 per KV head).
+ * rounded up to a multiple of 4, of 8 without rho or above 4 per KV head).  With
+ * wacc, scratch and the launch that adds the weights go by the table's slots, not
+ * by the lengths: a table as wide as the sequences need costs least.
  */
 PARALLAX_API int parallax_decode_paged_q8(const void *q, const void *rho, const void *kpages, const void *vpages,
                                           const signed char *kexp, const signed char *vexp, const int *block_table,
@@ -387,7 +389,13 @@ PARALLAX_API int parallax_kv_append(const void *k, const void *v, const long lon
  * stay: the newest min(recent, n), and of the others those with the largest
  * wacc (equal weights: the lower position first; NaN as -inf).  In their order
  * they become tokens 0 .. n-1 of the pages that new_table names; the pages of
- * block_table are only read, so the caller gives those back afterwards.
+ * block_table are only read, so the caller gives those back afterwards.  A
+ * sequence under the budget moves whole.
+ *
+ * Weights come from decode steps alone, and the append starts new tokens at 0: an
+ * eviction right after a prompt sees equal weights and keeps the newest `recent`
+ * and the first of the prompt.  For any other choice decode some steps first, or
+ * write weights of your own into wacc.
  *
  *   new_table   : DEVICE int32 [B, new_max_pages]: pages that no entry of
  *                 block_table reaches.  Another array than block_table.

@@ -406,6 +406,9 @@ def parallax_kv_evict(kpages, vpages, block_table, seqlens, wacc, new_table, bud
     block_table reaches).  Returns (new_seqlens int32 [B], kept int32 [B, Hkv, budget]: old positions,
     new_wacc fp32 [B, Hkv, new_max_pages * page_size]); kept and new_wacc are written up to each
     sequence's new length, and start as zero when they are allocated here.
+
+    Weights come from decode steps: after a prompt alone all are 0, and the newest and the first
+    tokens of the prompt stay.
     """
     args = (kpages, vpages, kexp, vexp, block_table, seqlens, wacc, new_table, int(budget), int(recent), new_seqlens,
             kept, new_wacc)

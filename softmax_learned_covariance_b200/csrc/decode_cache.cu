@@ -28,8 +28,8 @@
 // Bound by the loads, and how they are issued decides their rate (B=64, 16 heads of
 // their own, 4096 tokens, d = 128, 1.07 GB; loads alone, merge launch included):
 // 16-byte cp.async in fragment order 205 us, in row order 196 us, TMA 167 us.  The
-// call takes 175 us, the kernel 166 (6.45 TB/s); B=16, 16 heads, 16384-32768 tokens
-// 259 us (6.2 TB/s of 6.57).  CTAs of equal ranges (decode_sched.h) end up to 20 %
+// call takes 175-180 us, the kernel 166-172 (6.2-6.45 TB/s); B=16, 16 heads, 16384-32768
+// tokens 257-265 us (6.1-6.3 TB/s of 6.57).  CTAs of equal ranges (decode_sched.h) end up to 20 %
 // apart, but the memory is saturated until the last one does: ranges taken from a
 // counter gained nothing.
 //
@@ -865,14 +865,8 @@ __global__ void __launch_bounds__(WARPS * 32, Shape<D, Q8, RHO, NT>::CTAS) k_dec
     }
 }
 
-// One launch after the decode (a programmatic dependent: its blocks are there when
-// the decode's CTAs leave).  The first blocks merge cut items and write y and lse:
-// one per CTA of the decode (the item that CTA starts but does not finish) with all
-// its heads, or, when items are few and have many parts (hpb = 1), one per item
-// and head; the others add the weights s = 2^(z - lse2) of ACC_TOKENS tokens of
-// one (b, kvh) to the accumulator, summed over the KV head's query heads in head
-// order (each token by one thread: the result does not depend on the schedule).
-// n / d for n < 2^31 by a multiplication (d >= 1): m = ceil(2^(31 + s) / d) with 2^s >= d.
+// n / d for n < 2^31 by a multiplication (d >= 1): m = ceil(2^(31 + s) / d) with 2^s >= d
+// (T. Granlund, P. L. Montgomery, Division by Invariant Integers using Multiplication, 1994).
 struct Divisor {
     unsigned d, m, s;
     explicit Divisor(int n) : d(n > 0 ? (unsigned)n : 1u), s(0) {
@@ -881,9 +875,17 @@ struct Divisor {
     }
     __device__ __forceinline__ unsigned of(unsigned n) const { return (unsigned)(((unsigned long long)n * m) >> (31 + s)); }
 };
+
 constexpr int FIN_THREADS = 256;
 constexpr int ACC_TOKENS = 1024;
 
+// One launch after the decode (a programmatic dependent: its blocks are there when
+// the decode's CTAs leave).  The first blocks merge cut items and write y and lse:
+// one per CTA of the decode (the item that CTA starts but does not finish) with all
+// its heads, or, when items are few and have many parts (hpb = 1), one per item
+// and head; the others add the weights s = 2^(z - lse2) of ACC_TOKENS tokens of
+// one (b, kvh) to the accumulator, summed over the KV head's query heads in head
+// order (each token by one thread: the result does not depend on the schedule).
 template <int D, bool RHO, int HEADS, typename Tout>
 __global__ void __launch_bounds__(FIN_THREADS, 4) k_decode_finish(
     Scratch ws, const int *__restrict__ seqlens, Tout *__restrict__ y, float *__restrict__ lse, float *__restrict__ wacc,
@@ -1105,7 +1107,10 @@ cudaError_t launch_t(const DecodeCacheArgs &A, const DecodeCacheScratch &sc, voi
         A.tmk, A.tmv, (const __nv_bfloat16 *)A.q, (const __nv_bfloat16 *)A.rho, A.kexp, A.vexp, A.seqlens, (Tout *)A.y, A.lse, A.B, A.Hq, htiles, sc.split, A.pg, ws, ctl);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (whole && A.wacc == nullptr)) return e;
-    // few items have many parts each and take a block per head, many items have two or three
+    // Few items have many parts each and take a block per head, many items have two or three and
+    // take one for all heads.  us, a block per head / per item: 8 items of 4096 tokens 14.5 / 18.7,
+    // 32 of 8192 26.8 / 28.3, 128 of 4096 39.1 / 39.5 (8 heads each 47.5 / 46.5), 256 of 4096
+    // 59.9 / 57.7, 512 of 4096 105.2 / 99.3.
     const int hpb = items >= 128 ? S::HEADS : 1;
     const int combine = whole ? 0 : (hpb == 1 ? items * S::HEADS : grid);
     const int acc_chunks = A.wacc ? (Tcap + ACC_TOKENS - 1) / ACC_TOKENS : 0;
