@@ -46,7 +46,7 @@ def bounds(q, rho, c, sl):
     16 products at a time, then the merges: (L / 32 + 64) 2^-23 of the sum of magnitudes.  All that is relative
     to a token's own contribution.  fp16 parts (e4m3) also have a smallest step: a weight and its product with a
     are off by 2^-25 where the largest contribution 2^ve weight so far is held at 2^10 or more, which is
-    2^-35 |code| of that; 2^-34 leaves the logarithm's rounding in.
+    2^-35 |code| of that (the bound takes twice as much).
     """
     B, Hq, d = q.shape
     G = Hq // c.Hkv
